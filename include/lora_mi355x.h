@@ -633,6 +633,126 @@ lora_status_t lora_sched_step(lora_sched_t sched, double now, int32_t capacity, 
 /* Requests waiting in the queue. */
 int32_t lora_sched_queued(lora_sched_t sched);
 
+/* ---------------------------------------------------------------------- */
+/* Paged key/value cache                                                   */
+/* ---------------------------------------------------------------------- */
+
+/* The step between the k/v projections and the o projection: keys and values
+ * of every sequence live in pages of one cache, a step appends its rows'
+ * keys and values (rotated by position on the way), and attention reads the
+ * pages back ("Serving many LoRA adapters" (blog.ecitis.org), section
+ * "Correctness across tenants": keys and values depend on the adapter, so a
+ * prefix is shared only between requests of one adapter and base revision;
+ * the caller's groups must keep to that).
+ *
+ * Element (page p, token t, key head h, dim d) of K and of V lies at
+ *     p * page_stride + t * token_stride + h * head_stride + d
+ * (elements), so [n_pages, n_kv_heads, page_size, head_dim], where one head's
+ * tokens of a page are neighbours, and [n_pages, page_size, n_kv_heads,
+ * head_dim] are both taken.  head_dim: 64 or 128, or 256 for bf16; page_size:
+ * a power of two (else LORA_E_UNSUPPORTED).  k and v are 16-byte aligned, and
+ * so are the strides times the element size.  The cache is the caller's. */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t page_stride, token_stride, head_stride;
+    lora_dtype_t dtype;
+    int32_t n_pages, page_size, n_kv_heads, head_dim;
+} lora_kv_cache_t;
+
+/* One step's sequences, the same for every layer.  Arrays are device.
+ *   row_off[n_seqs + 1]  rows of sequence s: row_off[s] .. row_off[s + 1] - 1
+ *                        (row_off[0] = 0, ascending; none is allowed);
+ *   kv_len[n_seqs]       its tokens in its own pages, this step's rows
+ *                        included (they are the last ones);
+ *   pages[n_seqs, ldp]   its page numbers: token t is in page
+ *                        pages[s, t / page_size];
+ *   max_rows, max_kv_len host bounds of a sequence's rows and tokens.  They
+ *                        size the launches and the workspace; rows and tokens
+ *                        past them are not computed or not seen.
+ * Groups of neighbouring sequences that share a prefix (n_groups = 0: none):
+ *   group_off[n_groups + 1]      sequences of group g (group_off[0] = 0);
+ *                                sequences past the last have no prefix;
+ *   prefix_len[n_groups], prefix_pages[n_groups, ldpp]  the prefix's tokens;
+ *   max_prefix_len, max_group_rows  host bounds, of all rows of a group.
+ * A row's position is its index among its sequence's own tokens plus the
+ * length of its prefix.  Rows past row_off[n_seqs] belong to no sequence:
+ * append writes zeros to q_out there, attention leaves o and lse as they
+ * are.  Contents that break these rules give unspecified values, but nothing
+ * outside the tensors named here is read or written. */
+typedef struct {
+    const int32_t* row_off;
+    const int32_t* kv_len;
+    const int32_t* pages;
+    int64_t ldp;
+    int32_t n_seqs, n_rows, max_rows, max_kv_len;
+    const int32_t* group_off;
+    const int32_t* prefix_len;
+    const int32_t* prefix_pages;
+    int64_t ldpp;
+    int32_t n_groups, max_prefix_len, max_group_rows;
+} lora_kv_batch_t;
+
+/* Rotary positions: row `position` of cos and sin ([n_pos, ld] fp32, device)
+ * holds rot_dim / 2 angles.  A head's first rot_dim elements are rotated in
+ * pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved != 0; the
+ * rest pass through.  rot_dim: a multiple of 16, at most head_dim. */
+typedef struct {
+    const float* cos;
+    const float* sin;
+    int64_t ld;
+    int32_t n_pos, rot_dim, interleaved;
+} lora_rope_t;
+
+/* For each row of the batch: rotate q and k by the row's position (rope NULL:
+ * not), write k and v to the row's place in the cache and q to q_out.  One
+ * launch; every element is computed in fp32 and rounded once.
+ *   q [n_rows, ldq], k and v [n_rows, ldk / ldv] of `dtype` (heads side by
+ *   side, as the projections leave them); q_out [n_rows, ldqo] of the cache's
+ *   type, which may be q itself when the types agree.  n_q_heads = 0: keys
+ *   and values only.
+ *   status (device, may be NULL) gets bit 0 set when a row has no place: its
+ *   index is negative or past the page table, its page number outside
+ *   [0, n_pages), or its position outside the rotary tables.  Nothing is
+ *   written to the cache for such a row, and zeros to q_out.  Two rows with
+ *   the same place are the caller's mistake. */
+lora_status_t lora_kv_append(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, const lora_rope_t* rope,
+                             lora_dtype_t dtype, const void* q, int64_t ldq, int32_t n_q_heads, const void* k,
+                             int64_t ldk, const void* v, int64_t ldv, void* q_out, int64_t ldqo, int32_t* status,
+                             hipStream_t stream);
+
+/* Attention of the batch's rows over the cache:
+ *     o = sum_k softmax_k(scale * q . k) v,  lse = log sum_k exp(scale * q . k)
+ * per row and query head; query heads h * G .. (h + 1) * G - 1 use key head h,
+ * G = n_q_heads / n_kv_heads.  A row at position p sees the tokens k of its
+ * sequence (and prefix) with k <= p and, with window > 0, k > p - window or
+ * k < n_sink (a sliding window whose first tokens stay visible).  A row that
+ * sees nothing gets o = 0 and lse = -infinity.  What a row does not see has
+ * no effect on it, infinities and NaN in the pages included.
+ *   q [n_rows, ldq] of the cache's type; o [n_rows, ldo] of o_dtype; lse
+ *   [n_rows, n_q_heads] fp32, may be NULL; scale > 0.
+ *   Scores, softmax statistics and sums are fp32; the weights are rounded to
+ *   the cache's type before the product with V, and o once at the end.
+ *   status (device, may be NULL) gets bit 0 set when a page number that some
+ *   row needs is outside [0, n_pages); its tokens are then not seen.
+ * Results do not depend on timing.  lora_attn_paged takes a batch without
+ * groups.  lora_attn_prefix takes one with groups: the prefix's keys and
+ * values are read once per group for all its rows, and each row's partial
+ * results over the prefix and over its own tokens are joined in fp32.
+ * The workspace (lora_attn_workspace, for either entry point and any window)
+ * holds partial results only; it needs no zero-filling, and any content is
+ * left in it. */
+lora_status_t lora_attn_workspace(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, int32_t n_q_heads,
+                                  size_t* bytes);
+lora_status_t lora_attn_paged(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, const void* q, int64_t ldq,
+                              int32_t n_q_heads, float scale, int32_t window, int32_t n_sink, void* o,
+                              lora_dtype_t o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+lora_status_t lora_attn_prefix(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, const void* q, int64_t ldq,
+                               int32_t n_q_heads, float scale, int32_t window, int32_t n_sink, void* o,
+                               lora_dtype_t o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws,
+                               size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

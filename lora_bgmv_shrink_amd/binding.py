@@ -49,6 +49,7 @@ EXPORTS = [
     "lora_decode_stream_q4",
     "lora_sched_create", "lora_sched_destroy", "lora_sched_submit", "lora_sched_step", "lora_sched_queued",
     "lora_layer_apply_noalloc", "lora_layer_q4_workspace", "lora_layer_apply_q4",
+    "lora_kv_append", "lora_attn_workspace", "lora_attn_paged", "lora_attn_prefix",
 ]
 
 
@@ -80,6 +81,26 @@ class SchedStepT(ctypes.Structure):
 class SegmentsT(ctypes.Structure):
     _fields_ = [("perm", ctypes.c_void_p), ("seg_ids", ctypes.c_void_p), ("seg_off", ctypes.c_void_p),
                 ("n_seg", ctypes.c_void_p), ("cap", ctypes.c_int32)]
+
+
+class KvCacheT(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride")] + \
+        [("dtype", ctypes.c_int)] + [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim")]
+
+
+class KvBatchT(ctypes.Structure):
+    _fields_ = [("row_off", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("ldp", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("n_seqs", "n_rows", "max_rows", "max_kv_len")] + \
+        [("group_off", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p),
+         ("ldpp", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("n_groups", "max_prefix_len", "max_group_rows")]
+
+
+class RopeT(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 def _load():
@@ -135,6 +156,10 @@ def _load():
         "lora_layer_apply_noalloc": (st, [p, p, i64, p, i64, st, p, p, i32, p, st, i64, st, p]),
         "lora_layer_q4_workspace": (st, [p, i32, p]),
         "lora_layer_apply_q4": (st, [p, p, i64, p, i64, p, i64, p, p, i32, p, st, i64, p, sz, p]),
+        "lora_kv_append": (st, [p, p, p, st, p, i64, i32, p, i64, p, i64, p, i64, p, p]),
+        "lora_attn_workspace": (st, [p, p, i32, p]),
+        "lora_attn_paged": (st, [p, p, p, i64, i32, ctypes.c_float, i32, i32, p, st, i64, p, p, p, sz, p]),
+        "lora_attn_prefix": (st, [p, p, p, i64, i32, ctypes.c_float, i32, i32, p, st, i64, p, p, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -506,6 +531,157 @@ def lora_merge_adapter(pool: Pool, W: torch.Tensor, adapter: int, w_layout: int,
     _check(_lib.lora_merge_adapter(pool.handle, int(adapter), _ptr(W), _ld(W), int(w_layout), float(sign),
                                    ctypes.c_void_p(_stream(W.device))), "lora_merge_adapter")
     return W
+
+
+# --------------------------------------------------------------------------
+# Paged key/value cache
+# --------------------------------------------------------------------------
+
+class KvCache:
+    """A paged cache over the caller's tensors ``k`` and ``v``, each seen as
+    [n_pages, page_size, n_kv_heads, head_dim] with equal strides (pages
+    stored [n_pages, n_kv_heads, page_size, head_dim], one head's tokens side
+    by side, are passed as ``t.transpose(1, 2)``).  Keeps the tensors alive."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        assert k.is_cuda and v.is_cuda and k.dim() == 4 and k.dtype == v.dtype and k.device == v.device
+        assert k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1, \
+            "k and v: one shape, equal strides, head_dim contiguous"
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = (int(n) for n in k.shape)
+        self.struct = KvCacheT(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), _dt(k.dtype),
+                               self.n_pages, self.page_size, self.n_kv_heads, self.head_dim)
+        self.ref = ctypes.addressof(self.struct)
+
+
+class KvBatch:
+    """One step's sequences (lora_kv_batch_t): int32 device tensors, and the
+    host bounds that size launches and workspaces.  The tensors are kept, so
+    their contents may be changed in place within the bounds."""
+
+    def __init__(self, row_off: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, n_rows: int, max_rows: int,
+                 max_kv_len: int, group_off: Optional[torch.Tensor] = None, prefix_len: Optional[torch.Tensor] = None,
+                 prefix_pages: Optional[torch.Tensor] = None, max_prefix_len: int = 0, max_group_rows: int = 0):
+        for t in (row_off, kv_len, pages, group_off, prefix_len, prefix_pages):
+            assert t is None or (t.is_cuda and t.dtype == torch.int32), "int32 device tensors"
+        for t in (row_off, kv_len, group_off, prefix_len):
+            assert t is None or (t.dim() == 1 and t.is_contiguous())
+        n_seqs = kv_len.numel()
+        assert row_off.numel() == n_seqs + 1 and pages.shape[0] == n_seqs
+        n_groups = 0 if group_off is None else group_off.numel() - 1
+        if n_groups:
+            assert prefix_len.numel() == n_groups and prefix_pages.shape[0] == n_groups
+        self.tensors = (row_off, kv_len, pages, group_off, prefix_len, prefix_pages)
+        self.n_seqs, self.n_rows, self.n_groups = n_seqs, int(n_rows), n_groups
+        ptr = [None if t is None else t.data_ptr() for t in self.tensors]
+        self.struct = KvBatchT(ptr[0], ptr[1], ptr[2], self._width(pages), n_seqs, self.n_rows, int(max_rows),
+                               int(max_kv_len), ptr[3], ptr[4], ptr[5], self._width(prefix_pages) if n_groups else 0,
+                               n_groups, int(max_prefix_len), int(max_group_rows))
+        self.ref = ctypes.addressof(self.struct)
+
+    @staticmethod
+    def _width(table: torch.Tensor) -> int:
+        # the row pitch is the width the library may index: a table is passed whole
+        assert table.dim() == 2 and table.is_contiguous(), "a contiguous page table"
+        return int(table.shape[1])
+
+
+class Rope:
+    """Rotary tables: ``cos`` and ``sin`` fp32 [n_pos, rot_dim / 2]."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
+        assert cos.is_cuda and cos.dtype == sin.dtype == torch.float32 and cos.shape == sin.shape
+        assert cos.dim() == 2 and cos.stride() == sin.stride() and cos.stride(1) == 1
+        self.cos, self.sin = cos, sin
+        self.struct = RopeT(cos.data_ptr(), sin.data_ptr(), cos.stride(0), cos.shape[0], 2 * cos.shape[1],
+                            int(bool(interleaved)))
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _heads(t: torch.Tensor, rows: int, d: int) -> int:
+    assert t.is_cuda and t.dim() == 2 and t.stride(1) == 1 and t.shape[0] == rows and t.shape[1] % d == 0, \
+        "expected [n_rows, heads * head_dim], row-major"
+    return t.shape[1] // d
+
+
+def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                   rope: Optional[Rope] = None, q_out: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Rotate the rows' q and k, write k and v into their pages and return
+    the rotated q in the cache's type (``q_out``, allocated when not given;
+    None without q)."""
+    n, d = batch.n_rows, cache.head_dim
+    assert k.dtype == v.dtype and _heads(k, n, d) == cache.n_kv_heads == _heads(v, n, d)
+    hq = 0
+    if q is not None:
+        hq = _heads(q, n, d)
+        assert q.dtype == k.dtype
+        if q_out is None:
+            q_out = torch.empty((n, hq * d), dtype=cache.dtype, device=q.device)
+        assert q_out.dtype == cache.dtype and _heads(q_out, n, d) == hq
+    assert status is None or status.dtype == torch.int32
+    st = _lib.lora_kv_append(cache.ref, batch.ref, None if rope is None else rope.ref, _dt(k.dtype),
+                             q.data_ptr() if hq else None, q.stride(0) if hq else 0, hq, k.data_ptr(), k.stride(0),
+                             v.data_ptr(), v.stride(0), q_out.data_ptr() if hq else None,
+                             q_out.stride(0) if hq else 0, None if status is None else status.data_ptr(),
+                             _stream(k.device))
+    if st:
+        _check(st, "lora_kv_append")
+    return q_out if hq else None
+
+
+def lora_attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> int:
+    v = ctypes.c_size_t()
+    _check(_lib.lora_attn_workspace(cache.ref, batch.ref, n_q_heads, ctypes.byref(v)), "lora_attn_workspace")
+    return v.value
+
+
+def attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> torch.Tensor:
+    """A workspace for either attention over this batch (or one with no
+    larger bounds), for calls that do not overlap in time."""
+    return torch.empty(lora_attn_workspace(cache, batch, n_q_heads), dtype=torch.uint8, device=cache.device)
+
+
+def _attn(fn, where: str, cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: float, window: int, n_sink: int,
+          o: Optional[torch.Tensor], o_dtype: Optional[torch.dtype], lse: Optional[torch.Tensor],
+          status: Optional[torch.Tensor], ws: Optional[torch.Tensor]) -> torch.Tensor:
+    n, d = batch.n_rows, cache.head_dim
+    hq = _heads(q, n, d)
+    assert q.dtype == cache.dtype, "q has the cache's type"
+    if o is None:
+        o = torch.empty((n, hq * d), dtype=o_dtype or cache.dtype, device=q.device)
+    assert _heads(o, n, d) == hq
+    if lse is not None:
+        assert lse.dtype == torch.float32 and lse.shape == (n, hq) and lse.is_contiguous()
+    assert status is None or status.dtype == torch.int32
+    if ws is None:
+        ws = attn_workspace(cache, batch, hq)
+    st = fn(cache.ref, batch.ref, q.data_ptr(), q.stride(0), hq, scale, window, n_sink, o.data_ptr(), _dt(o.dtype),
+            o.stride(0), None if lse is None else lse.data_ptr(), None if status is None else status.data_ptr(),
+            ws.data_ptr(), ws.numel(), _stream(q.device))
+    if st:
+        _check(st, where)
+    return o
+
+
+def lora_attn_paged(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0, n_sink: int = 0,
+                    o: Optional[torch.Tensor] = None, o_dtype: Optional[torch.dtype] = None,
+                    lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of the batch's rows over their pages; ``lse`` [n_rows,
+    n_q_heads] fp32 is filled when given."""
+    return _attn(_lib.lora_attn_paged, "lora_attn_paged", cache, batch, q, scale, window, n_sink, o, o_dtype, lse,
+                 status, ws)
+
+
+def lora_attn_prefix(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0, n_sink: int = 0,
+                     o: Optional[torch.Tensor] = None, o_dtype: Optional[torch.dtype] = None,
+                     lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """lora_attn_paged for a batch whose groups of sequences share a prefix,
+    whose keys and values are read once per group."""
+    return _attn(_lib.lora_attn_prefix, "lora_attn_prefix", cache, batch, q, scale, window, n_sink, o, o_dtype, lse,
+                 status, ws)
 
 
 # --------------------------------------------------------------------------

@@ -19,7 +19,8 @@ LIB_NAME = "liblora_mi355x.so"
 # LORA_MI355X_LIB names another build of the library to load (the host-code
 # sanitizer run's instrumented copy); the default is the in-tree build
 LIB_PATH = os.environ.get("LORA_MI355X_LIB") or os.path.join(HERE, LIB_NAME)
-SOURCES = ["api.hip", "segments.hip", "bgmv.hip", "mfma.hip", "decode.hip", "merge.hip", "cache.hip", "rows.hip", "sched.cpp"]
+SOURCES = ["api.hip", "segments.hip", "bgmv.hip", "mfma.hip", "decode.hip", "merge.hip", "cache.hip", "rows.hip", "sched.cpp",
+           "kv.hip", "attn.hip", "kv_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,123 @@
+"""CPU checks of the paged cache's entry points: what they refuse, before any device work."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+FAKE, MIS = 0x1000, 0x1008   # never dereferenced: every call here ends in the checks
+
+
+def structs():
+    from lora_bgmv_shrink_amd import binding as b
+    cache = b.KvCacheT(FAKE, FAKE, 2 * 16 * 64, 64, 16 * 64, b.LORA_BF16, 8, 16, 2, 64)
+    batch = b.KvBatchT(FAKE, FAKE, FAKE, 4, 3, 5, 4, 60, None, None, None, 0, 0, 0, 0)
+    rope = b.RopeT(FAKE, FAKE, 32, 100, 64, 0)
+    return b, cache, batch, rope
+
+
+def attn(b, cache, batch, fn="lora_attn_paged", q=FAKE, ldq=256, hq=4, scale=0.1, window=0, n_sink=0, o=FAKE, o_dtype=1,
+         ldo=256, lse=None, ws=FAKE, ws_bytes=0):
+    return getattr(b.library(), fn)(None if cache is None else ctypes.addressof(cache),
+                                    None if batch is None else ctypes.addressof(batch), q, ldq, hq, scale, window,
+                                    n_sink, o, o_dtype, ldo, lse, None, ws, ws_bytes, None)
+
+
+def append(b, cache, batch, rope, dtype=1, q=FAKE, ldq=256, hq=4, k=FAKE, ldk=128, v=FAKE, ldv=128, qo=FAKE, ldqo=256):
+    return b.library().lora_kv_append(ctypes.addressof(cache), ctypes.addressof(batch),
+                                      None if rope is None else ctypes.addressof(rope), dtype, q, ldq, hq, k, ldk, v,
+                                      ldv, qo, ldqo, None, None)
+
+
+@pytest.mark.parametrize("field,value,unsupported", [
+    ("k", 0, False), ("k", MIS, True), ("dtype", 7, False), ("n_pages", 0, False), ("page_size", 12, True),
+    ("page_size", 0, False), ("n_kv_heads", 0, False), ("head_dim", 80, True), ("head_dim", 0, False),
+    ("token_stride", 65, True), ("page_stride", -16, False)])
+def test_cache_refusals(field, value, unsupported):
+    b, cache, batch, rope = structs()
+    setattr(cache, field, value)
+    want = b.LORA_E_UNSUPPORTED if unsupported else b.LORA_E_INVALID
+    assert attn(b, cache, batch) == want
+    assert append(b, cache, batch, rope) == want
+    n = ctypes.c_size_t()
+    assert b.library().lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), 4, ctypes.byref(n)) == want
+
+
+def test_head_dim_256_is_bf16_only():
+    b, cache, batch, _ = structs()
+    cache.head_dim, cache.dtype = 256, b.LORA_F32
+    assert attn(b, cache, batch, ldq=1024, ldo=1024) == b.LORA_E_UNSUPPORTED
+
+
+@pytest.mark.parametrize("field,value", [("row_off", 0), ("kv_len", 0), ("pages", 0), ("n_rows", -1), ("n_seqs", -1),
+                                         ("max_rows", -1), ("ldp", -1), ("n_groups", -1), ("pages", 0x1002)])
+def test_batch_refusals(field, value):
+    b, cache, batch, rope = structs()
+    setattr(batch, field, value)
+    assert attn(b, cache, batch) == b.LORA_E_INVALID
+    assert append(b, cache, batch, rope) == b.LORA_E_INVALID
+
+
+def test_attention_refusals():
+    b, cache, batch, _ = structs()
+    I, U = b.LORA_E_INVALID, b.LORA_E_UNSUPPORTED
+    assert attn(b, None, batch) == I and attn(b, cache, None) == I
+    assert attn(b, cache, batch, hq=3) == I and attn(b, cache, batch, hq=0) == I     # not a multiple of the key heads
+    assert attn(b, cache, batch, window=-1) == I and attn(b, cache, batch, n_sink=-1) == I
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        assert attn(b, cache, batch, scale=scale) == I
+    assert attn(b, cache, batch, q=None) == I and attn(b, cache, batch, o=None) == I
+    assert attn(b, cache, batch, o_dtype=5) == I
+    assert attn(b, cache, batch, ldq=255) == I and attn(b, cache, batch, ldo=255) == I
+    assert attn(b, cache, batch, q=MIS) == U and attn(b, cache, batch, ldq=260) == U and attn(b, cache, batch, ldo=260) == U
+    assert attn(b, cache, batch, lse=0x1002) == U
+    # groups go with one entry point and not with the other
+    assert attn(b, cache, batch, fn="lora_attn_prefix") == I
+    batch.group_off = batch.prefix_len = batch.prefix_pages = FAKE
+    batch.n_groups, batch.ldpp, batch.max_prefix_len, batch.max_group_rows = 1, 4, 60, 5
+    assert attn(b, cache, batch) == I
+    assert attn(b, cache, batch, fn="lora_attn_prefix") == b.LORA_E_WORKSPACE
+    n = ctypes.c_size_t()
+    assert b.library().lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), 4, ctypes.byref(n)) == 0
+    assert n.value > 0
+    assert attn(b, cache, batch, fn="lora_attn_prefix", ws=MIS, ws_bytes=n.value) == b.LORA_E_WORKSPACE
+    assert attn(b, cache, batch, fn="lora_attn_prefix", ws_bytes=n.value - 1) == b.LORA_E_WORKSPACE
+    batch.prefix_len = None
+    assert attn(b, cache, batch, fn="lora_attn_prefix") == I
+
+
+def test_workspace_covers_every_window():
+    """The size does not depend on the window, so it bounds what any window's plan takes."""
+    b, cache, batch, _ = structs()
+    lib = b.library()
+    cache.n_kv_heads, batch.n_seqs, batch.n_rows, batch.max_rows, batch.max_kv_len = 2, 9, 300, 200, 5000
+    n = ctypes.c_size_t()
+    assert lib.lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), 4, ctypes.byref(n)) == 0
+    for window in (0, 1, 63, 64, 100, 1000, 4999, 2 ** 31 - 1):
+        # one byte less is refused whatever the window: all calls check the same size
+        assert attn(b, cache, batch, window=window, n_sink=4, ws_bytes=n.value - 1) == b.LORA_E_WORKSPACE
+
+
+def test_append_refusals():
+    b, cache, batch, rope = structs()
+    I, U = b.LORA_E_INVALID, b.LORA_E_UNSUPPORTED
+    assert append(b, cache, batch, rope, dtype=9) == I
+    assert append(b, cache, batch, rope, k=None) == I and append(b, cache, batch, rope, v=None) == I
+    assert append(b, cache, batch, rope, q=None) == I and append(b, cache, batch, rope, qo=None) == I
+    assert append(b, cache, batch, rope, ldk=127) == I and append(b, cache, batch, rope, ldq=255) == I
+    assert append(b, cache, batch, rope, k=MIS) == U and append(b, cache, batch, rope, ldv=129) == U
+    assert append(b, cache, batch, rope, ldqo=258) == U
+    for field, value, want in (("cos", 0, I), ("rot_dim", 0, I), ("rot_dim", 80, I), ("rot_dim", 24, U), ("n_pos", 0, I),
+                               ("ld", 31, I), ("ld", 33, U), ("sin", MIS, U)):
+        _, _, _, r = structs()
+        setattr(r, field, value)
+        assert append(b, cache, batch, r) == want, (field, value)
+
+
+def test_no_rows_is_a_no_op():
+    b, cache, batch, rope = structs()
+    batch.n_rows = batch.max_rows = 0
+    assert append(b, cache, batch, rope) == b.LORA_OK
+    assert attn(b, cache, batch) in (b.LORA_OK, b.LORA_E_WORKSPACE)
+    batch.n_seqs = 0
+    assert attn(b, cache, batch, ws=None) == b.LORA_OK
