@@ -650,8 +650,9 @@ int32_t lora_sched_queued(lora_sched_t sched);
  * (elements), so [n_pages, n_kv_heads, page_size, head_dim], where one head's
  * tokens of a page are neighbours, and [n_pages, page_size, n_kv_heads,
  * head_dim] are both taken.  head_dim: 64 or 128, or 256 for bf16; page_size:
- * a power of two (else LORA_E_UNSUPPORTED).  k and v are 16-byte aligned, and
- * so are the strides times the element size.  The cache is the caller's. */
+ * a power of two with page_size * token_stride < 2^30 (else
+ * LORA_E_UNSUPPORTED).  k and v are 16-byte aligned, and so are the strides
+ * times the element size.  The cache is the caller's. */
 typedef struct {
     void* k;
     void* v;

@@ -23,6 +23,7 @@ namespace {
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x8_t __attribute__((ext_vector_type(8)));
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -89,6 +90,16 @@ template <> struct Op<float> {
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// the larger of two, the other one if one is NaN (fmaxf would first quiet
+// both operands, an instruction each, for products of the matrix cores)
+__device__ __forceinline__ float max_of(float a, float b) {
+    return __builtin_amdgcn_fmed3f(a, b, __builtin_inff());
+}
+// The softmax's reference score m is not the largest score so far but one
+// that no score exceeds by more than this (in log2 units): weights stay below
+// 2^8, where fp32 and bf16 are as exact as below 1, and most tiles need no
+// rescaling of O.
+constexpr float kSlack = 8.f;
 
 // A staged tile of keys or values: rows of D elements as they lie, 16-byte
 // pieces permuted inside a row (or a pair of rows when a row is 128 bytes) so
@@ -103,31 +114,36 @@ struct Tile {
         return key * RB + ((piece ^ x) << 4);
     }
     // values, bf16: a transpose read takes 32 bytes of each of 4 rows per 16
-    // lanes, 8 or 16 rows in all; fp32: 64 neighbouring bytes of rows 4 apart
+    // lanes, 8 or 16 rows in all; fp32: 64 or 128 neighbouring bytes of rows 4 apart
     static __device__ __forceinline__ int v_at(int key, int piece) {
-        const int x = sizeof(T) == 4 ? ((key >> 2) & 3) << 2 : RB == 128 ? ((key >> 1) & 3) << 1 : (key & 7) << 1;
+        const int x = sizeof(T) == 4 ? ((key >> 2) & 1) << 2 : RB == 128 ? ((key >> 1) & 3) << 1 : (key & 7) << 1;
         return key * RB + ((piece ^ x) << 4);
     }
     static __device__ __forceinline__ int v_elem(int key, int dim) {
         const int byte = dim * (int)sizeof(T);
         return v_at(key, byte >> 4) + (byte & 15);
     }
-    // the operand holding, for dimension `dim` (this lane's row of V^T), keys
-    // k0 .. k0 + 3 and k1 .. k1 + 3.  l16: lane % 16; dim is dim0 + l16.
-    static __device__ __forceinline__ typename Op<T>::frag v_frag(const uint8_t* sv, int k0, int k1, int dim0, int l16) {
+    // The operand holding, for one dimension per lane (this lane's row of
+    // V^T), four keys from k + K0 and four from k + K1 (K0, K1 multiples of
+    // 8), k = the lane's first key: v_base gives the lane's offset for k and
+    // dimensions dim0 .. dim0 + 15, the rest is an immediate.  l16: lane % 16.
+    static __device__ __forceinline__ int v_base(int k, int dim0, int l16) {
+        if constexpr (sizeof(T) == 2) return v_elem(k + (l16 >> 2), dim0 + (l16 & 3) * 4);
+        else return v_elem(k, dim0 + l16);
+    }
+    template <int K0, int K1>
+    static __device__ __forceinline__ typename Op<T>::frag v_frag(const uint8_t* at) {
+        static_assert(K0 % 8 == 0 && K1 % 8 == 0, "the permutation repeats every 8 keys");
         if constexpr (sizeof(T) == 2) {
-            const int r = l16 >> 2, dim = dim0 + (l16 & 3) * 4;
-            const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) i16x4_t*)(sv + v_elem(k0 + r, dim)));
-            const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) i16x4_t*)(sv + v_elem(k1 + r, dim)));
+            const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(at + K0 * RB));
+            const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(at + K1 * RB));
             return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             f32x8_t f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                f[e] = *(const float*)(sv + v_elem(k0 + e, dim0 + l16));
-                f[e + 4] = *(const float*)(sv + v_elem(k1 + e, dim0 + l16));
+                f[e] = *(const float*)(at + (K0 + e) * RB);
+                f[e + 4] = *(const float*)(at + (K1 + e) * RB);
             }
             return f;
         }
@@ -177,12 +193,11 @@ __device__ __forceinline__ int table_keys(int len, int64_t ld, int shift) {
     return (int)max((int64_t)0, min((int64_t)len, min(ld << shift, (int64_t)0x7fffff00)));
 }
 
-template <int KIND>
-__device__ inline Prob load_prob(const AttnArgs& a, int p) {
+__device__ inline Prob load_prob(const AttnArgs& a, int kind, int p) {
     const KvBatchDev& B = a.B;
     Prob P;
     int r0, r1;
-    if (KIND == 0) {
+    if (kind == 0) {
         r0 = B.row_off[p];
         r1 = B.row_off[p + 1];
     } else {
@@ -192,10 +207,10 @@ __device__ inline Prob load_prob(const AttnArgs& a, int p) {
     }
     P.r0 = min(max(r0, 0), B.n_rows);
     const int nr = min(max(r1, P.r0), B.n_rows) - P.r0;
-    P.nr = min(nr, a.part[KIND].max_rows);
-    if (KIND == 0) {
+    P.nr = min(nr, a.part[kind].max_rows);
+    P.key0 = 0;
+    if (kind == 0) {
         const int n = max(B.kv_len[p], 0);
-        P.key0 = 0;
         if (B.n_groups) {
             const int g = find_run(B.group_off, B.n_groups, p);
             if (g < B.n_groups) P.key0 = max(B.prefix_len[g], 0);
@@ -206,13 +221,16 @@ __device__ inline Prob load_prob(const AttnArgs& a, int p) {
         P.tbl = B.pages + (int64_t)p * B.ldp;
     } else {
         const int n = max(B.prefix_len[p], 0);
-        P.key0 = 0;
         P.len = table_keys(min(n, a.part[1].max_len), B.ldpp, a.C.page_shift);
         P.pos0 = n;
         P.pos1 = 0x7ffffffe;
         P.tbl = B.prefix_pages + (int64_t)p * B.ldpp;
     }
     return P;
+}
+__device__ __forceinline__ int problems(const AttnArgs& a, int kind) { return kind == 0 ? a.B.n_seqs : a.B.n_groups; }
+__device__ __forceinline__ bool is_few(const AttnArgs& a, const Prob& P) {
+    return (int64_t)P.nr * a.share <= ATTN_FEW_COLS;
 }
 
 // Tiles of KB keys that rows at positions p_lo .. p_hi see some key of: tiles
@@ -343,6 +361,81 @@ __device__ __forceinline__ float lse_of(const AttnArgs& a, float m, float l) {
 }
 
 // ---------------------------------------------------------------------------
+// Requests of keys and values
+// ---------------------------------------------------------------------------
+
+// 16 bytes; ONCE: no other workgroup reads them, so they pass the caches by
+// (a read stream of this shape reaches 6.5 TB/s so, and 5.9 through L2)
+template <bool ONCE>
+__device__ __forceinline__ u32x4_t piece_at(const void* p) {
+    if constexpr (ONCE) return __builtin_nontemporal_load((const u32x4_t*)p);
+    return *(const u32x4_t*)p;
+}
+
+// Where the wave-wide loads of N x `rows` neighbouring keys start: page number
+// `id` holds that of key `lane` of the tile (page 0 in the place of none).
+// PAGED: a load's rows lie in one page (page_size >= the rows of a load), so
+// its base is scalar; otherwise every lane follows its own key's page.
+template <typename T, int D, int NL, int STEP, bool PAGED, bool ONCE>
+__device__ __forceinline__ void request(const AttnArgs& a, int id, int base, int row0, int h, int lane, u32x4_t (&rk)[NL],
+                                        u32x4_t (&rv)[NL]) {
+    using TL = Tile<T, D>;
+    const int mask = (1 << a.C.page_shift) - 1;
+    const int r = lane / TL::LPR, piece = (lane % TL::LPR) * (16 / (int)sizeof(T));
+    const int64_t hs = (int64_t)h * a.C.head_stride;
+    if constexpr (PAGED) {
+        const uint32_t lo = (uint32_t)(r * (int)a.C.token_stride + piece);
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int row = row0 + j * STEP;   // uniform
+            const int64_t page = __builtin_amdgcn_readlane(id, row);
+            const int64_t off = page * a.C.page_stride + (int64_t)(((base + row) & mask) * (int)a.C.token_stride) + hs;
+            rk[j] = piece_at<ONCE>((const T*)a.C.k + off + lo);
+            rv[j] = piece_at<ONCE>((const T*)a.C.v + off + lo);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int row = row0 + j * STEP + r;
+            const int64_t off = (int64_t)__shfl(id, row, 64) * a.C.page_stride +
+                                (int64_t)((base + row) & mask) * a.C.token_stride + hs + piece;
+            rk[j] = piece_at<ONCE>((const T*)a.C.k + off);
+            rv[j] = piece_at<ONCE>((const T*)a.C.v + off);
+        }
+    }
+}
+template <int NL>
+__device__ __forceinline__ void hide_rows(u32x4_t (&rv)[NL], uint64_t bits, int row0, int step) {
+#pragma unroll
+    for (int j = 0; j < NL; ++j)
+        if (!((bits >> (row0 + j * step)) & 1)) rv[j] = u32x4_t{0u, 0u, 0u, 0u};
+}
+template <typename T>
+__device__ __forceinline__ bool odd_piece(const u32x4_t& v) {
+    if constexpr (sizeof(T) == 4) {
+        auto bad = [](uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; };
+        return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+    } else {
+        auto bad = [](uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; };
+        return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
+    }
+}
+
+// Whether a lane's column sees key k of a tile: `see` and `from` are the last
+// and first such k by position (first tokens: k < sink), bit k of `bits` is
+// set for keys that exist.
+struct Sees {
+    int see, from, sink;
+    __device__ __forceinline__ Sees(const AttnArgs& a, int col_pos, int lo) {
+        see = col_pos - lo;
+        from = a.window > 0 ? see - a.window + 1 : -0x7fffffff;
+        sink = a.window > 0 ? a.n_sink - lo : 0;
+    }
+    // (no branches: one test after the other would make a jump of each)
+    __device__ __forceinline__ bool at(int k) const { return (k <= see) & ((k >= from) | (k < sink)); }
+};
+
+// ---------------------------------------------------------------------------
 // Few query columns (decode): the keys are split
 // ---------------------------------------------------------------------------
 
@@ -352,14 +445,13 @@ __device__ __forceinline__ float lse_of(const AttnArgs& a, float m, float l) {
 //
 // A work unit is 128 keys of one (problem, key head); each of the four waves
 // takes 32 of them through LDS of its own (no barrier), with the next unit's
-// pieces in flight in registers and the unit after's page numbers behind
-// them.  SHARED: the units of all problems are dealt to the workgroups in
-// equal runs, whatever the lengths; a run's first and last (problem, head)
-// may be partial and go to slots that the join adds.  Otherwise a workgroup
-// takes one (problem, head) whole.
-template <typename T, int D, int KIND, bool SHARED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) * D <= 256 ? 2 : 1)))
-void k_attn_few(AttnArgs a) {
+// pieces in flight in registers and the unit after's page numbers before
+// them.  Shared form (few = 2): the units of all problems are dealt to the
+// workgroups in equal runs, whatever the lengths; a run's first and last
+// (problem, head) may be partial and go to slots that the join adds.
+// Otherwise a workgroup takes one (problem, head) whole.
+template <typename T, int D, bool PAGED>
+__device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block, int blocks, uint8_t* stage, int* sh) {
     using TL = Tile<T, D>;
     using O = Op<T>;
     constexpr int KW = ATTN_FEW_KEYS / 4;            // keys of a wave's unit
@@ -367,313 +459,283 @@ void k_attn_few(AttnArgs a) {
     constexpr int RPL = 64 / TL::LPR;                // rows one load covers
     constexpr int WB = 2 * KW * TL::RB;              // LDS bytes of a wave
     constexpr int OP = D + 4;                        // fp32 pitch of a wave's O at the end
-    static_assert(16 * OP * 4 <= WB, "O fits the wave's stage");
-    __shared__ __attribute__((aligned(16))) uint8_t stage[4 * WB];
-    __shared__ float sM[4][16], sL[4][16];
-    __shared__ int sh[8];
+    static_assert(16 * OP * 4 + 128 <= WB, "O and its statistics fit the wave's stage");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g4 = lane >> 4;
     const int hkv = a.C.n_kv_heads;
-    const AttnPart& W = a.part[KIND];
-    const int n_prob = KIND == 0 ? a.B.n_seqs : a.B.n_groups;
+    const AttnPart& W = a.part[kind];
+    const bool shared = W.few == 2;
+    const int n_prob = problems(a, kind);
     uint8_t* sk = stage + wave * WB;
     uint8_t* sv = sk + KW * TL::RB;
     const float c = a.scale * kLog2e;
+    const float kInf = __builtin_inff();
+    const float slack = kSlack / c;
+    int vb[D / 16];   // this lane's place in the stage of values, per 16 dimensions
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) vb[t] = TL::v_base(4 * g4, t * 16, l16);
 
-    // units of a problem, per key head
     auto range_of = [&](const Prob& P) __attribute__((always_inline)) {
-        if (P.nr == 0 || P.nr * a.share > ATTN_FEW_COLS) return Range{0, 0, 0};
+        if (P.nr == 0 || !is_few(a, P)) return Range{0, 0, 0};
         return key_tiles<ATTN_FEW_KEYS>(a, P, P.pos0, P.pos1);
     };
 
-    struct At {
-        int p, h, i;
-        Prob P;
-        Range R;
-    } L;
-    int u, u1;      // this workgroup's units [u, u1)
+    int p, h, i;    // the piece worked on: problem, key head, first unit of it
+    Prob P;
+    Range R;
+    int u = 0, u1;  // this workgroup's units [u, u1)
     int64_t total = 0, wgs = 1;   // all units, and the workgroups that have some
-    if (SHARED) {
-        auto units = [&](int p) { return range_of(load_prob<KIND>(a, p)).n * hkv; };
+    if (shared) {
+        auto units = [&](int q) { return range_of(load_prob(a, kind, q)).n * hkv; };
         total = sum_units(n_prob, units, tid, sh);
-        wgs = min((int64_t)gridDim.x, total);   // no run between a first and a last one is empty
-        if (blockIdx.x >= wgs) return;
-        u = (int)(blockIdx.x * total / wgs);
-        u1 = (int)((blockIdx.x + 1) * total / wgs);
+        wgs = min((int64_t)blocks, total);   // no run between a first and a last one is empty
+        if (block >= wgs) return;
+        u = (int)(block * total / wgs);
+        u1 = (int)((block + 1) * total / wgs);
         int base = 0;
-        if (!locate(n_prob, u, units, tid, sh, L.p, base)) return;
-        L.P = load_prob<KIND>(a, L.p);
-        L.R = range_of(L.P);
-        const int rem = u - base;
-        L.h = rem / L.R.n;
-        L.i = rem - L.h * L.R.n;
+        if (!locate(n_prob, u, units, tid, sh, p, base)) return;
+        P = load_prob(a, kind, p);
+        R = range_of(P);
+        h = (u - base) / R.n;
+        i = u - base - h * R.n;
     } else {
-        L.p = blockIdx.x / hkv;
-        L.h = blockIdx.x - L.p * hkv;
-        L.i = 0;
-        L.P = load_prob<KIND>(a, L.p);
-        L.R = range_of(L.P);
-        u = 0;
-        u1 = L.R.n;
-        if (L.P.nr == 0 || L.P.nr * a.share > ATTN_FEW_COLS) return;   // no rows, or the tiled kernel's
+        p = block / hkv;
+        h = block - p * hkv;
+        i = 0;
+        P = load_prob(a, kind, p);
+        if (P.nr == 0 || !is_few(a, P)) return;   // no rows, or the tiled form's
+        R = range_of(P);
+        u1 = R.n;
     }
 
-    // m, l of this lane's column (l: this lane's keys only, until the end)
-    float m = -__builtin_inff(), l = 0.f;
-    f32x4_t acc[D / 16];
-    typename O::frag qf[D / 32];
+    const int first = u;
+    while (true) {
+        const int n = min(R.n - i, u1 - u);   // units of this piece (0: rows that see no key)
+        // m, l of this lane's column (l: this lane's keys only, until the end)
+        float m = -kInf, l = 0.f;
+        f32x4_t acc[D / 16];
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        typename O::frag qf[D / 32];
+        int col_pos = -1;   // position of this lane's column, -1: no column
+        {
+            const int j = l16 / a.share;
+            const bool there = l16 < P.nr * a.share;
+            const T* q = (const T*)a.q + (int64_t)(P.r0 + j) * a.ldq + (int64_t)(h * a.share + l16 - j * a.share) * D;
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) qf[s] = there ? O::load(q + s * 32 + g4 * 8) : O::zero();
+            if (there) col_pos = kind == 0 ? P.pos0 + j : a.window > 0 ? row_position(a, P.r0 + j) : P.pos1;
+        }
 
-    // Joins the four waves' results for (p, h) and writes them.
-    auto finish = [&](const At& X, bool whole, int slot) __attribute__((always_inline)) {
+        // page number of key `lane` of the wave's unit x (lanes 0 .. 31), -1: none
+        auto load_id = [&](int x) __attribute__((always_inline)) {
+            const int key = R.tile(x) * ATTN_FEW_KEYS + wave * KW + lane;
+            return lane < KW && key < P.len ? P.tbl[key >> a.C.page_shift] : -1;
+        };
+        u32x4_t rk[NL], rv[NL];
+        // requests the wave's pieces of unit x; the answer's bit k says whether
+        // any column sees key k (the others are read from page 0 and not used)
+        auto load_kv = [&](int x, int id) __attribute__((always_inline)) {
+            const int base = R.tile(x) * ATTN_FEW_KEYS + wave * KW;
+            const int key = base + lane, at = P.key0 + key;
+            const bool page_ok = id >= 0 && id < a.C.n_pages;
+            bool seen = lane < KW && key < P.len && at <= P.pos1;
+            if (a.window > 0) seen = seen && (at > P.pos0 - a.window || at < a.n_sink);
+            if (seen && !page_ok && a.status) flag_bad_id(a.status);
+            request<T, D, NL, RPL, PAGED, true>(a, page_ok ? id : 0, base, 0, h, lane, rk, rv);
+            return (uint32_t)__ballot(seen && page_ok);
+        };
+        auto compute = [&](int x, uint32_t bits, bool all_see, bool odd) __attribute__((always_inline)) {
+            f32x4_t s[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks) {
+                s[0] = O::mma16(TL::k_frag(sk, l16, ks * 32 + g4 * 8), qf[ks], s[0]);
+                s[1] = O::mma16(TL::k_frag(sk, 16 + l16, ks * 32 + g4 * 8), qf[ks], s[1]);
+            }
+            // element r of s[t]: key 16 t + 4 g4 + r, this lane's column
+            const int lo = P.key0 + R.tile(x) * ATTN_FEW_KEYS + wave * KW;
+            if (!all_see) {
+                asm volatile("");   // a branch: most tiles need no mask
+                const Sees S(a, col_pos, lo + 4 * g4);
+                const uint32_t mine = bits >> (4 * g4);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        s[t][r] = S.at(16 * t + r) & ((mine >> (16 * t + r)) & 1u) ? s[t][r] : -kInf;
+            }
+            float top = max_of(max_of(max_of(s[0][0], s[0][1]), max_of(s[0][2], s[0][3])),
+                               max_of(max_of(s[1][0], s[1][1]), max_of(s[1][2], s[1][3])));
+            top = max_of(top, __shfl_xor(top, 16, 64));
+            top = max_of(top, __shfl_xor(top, 32, 64));
+            if (__ballot(top > m + slack)) {
+                const bool up = top > m + slack;   // a column's own matter: its neighbours do not change its bits
+                const float f = up ? exp2_fast((m - top) * c) : 1.f;   // from -infinity: 0
+                l *= f;
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) acc[t] *= f;
+                if (up) m = top;
+            }
+            const float mc = m == -kInf ? 0.f : m * c;
+            f32x8_t w;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                w[r] = exp2_fast(s[0][r] * c - mc);
+                w[4 + r] = exp2_fast(s[1][r] * c - mc);
+            }
+            l += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+            const typename O::frag pf = O::round(w);
+            if (!odd) {
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t)
+                    acc[t] = O::mma16(TL::template v_frag<0, 16>(sv + vb[t]), pf, acc[t]);
+                return;
+            }
+            asm volatile("");
+            // Infinities or NaN among values that some rows do not see: they
+            // are left out of the product (0 times them is NaN) and added to
+            // the columns that see them.
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                typename O::frag vf = TL::template v_frag<0, 16>(sv + vb[t]);
+                O::clean(vf);
+                acc[t] = O::mma16(vf, pf, acc[t]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const Sees S(a, col_pos, lo);
+            for (int k = 0; k < KW; ++k) {
+                const int r = (k & 3) + 4 * (k >> 4);
+                float wk = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e == r) wk = w[e];
+                wk = __shfl(wk, ((k >> 2) & 3) * 16 + l16, 64);
+                if (!S.at(k) || !((bits >> k) & 1)) continue;
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = TL::v_one(sv, k, t * 16 + g4 * 4 + e);
+                        if (non_finite(y)) acc[t][e] += wk * y;
+                    }
+            }
+        };
+
+        if (n > 0) {
+            uint32_t bits = load_kv(i, load_id(i));
+            int id = n > 1 ? load_id(i + 1) : -1;
+            for (int x = i; x < i + n; ++x) {
+                const int lo = P.key0 + R.tile(x) * ATTN_FEW_KEYS + wave * KW;
+                const bool all_see = bits == 0xffffffffu && lo + KW - 1 <= P.pos0 &&
+                                     (a.window == 0 || lo > P.pos1 - a.window);
+                bool odd = false;
+                if (bits != 0xffffffffu) hide_rows<NL>(rv, bits, lane / TL::LPR, RPL);
+                if (!all_see && P.nr > 1) {
+#pragma unroll
+                    for (int j = 0; j < NL; ++j) odd |= odd_piece<T>(rv[j]);
+                    odd = __ballot(odd) != 0;
+                }
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    const int row = j * RPL + lane / TL::LPR, piece = lane % TL::LPR;
+                    *(u32x4_t*)(sk + TL::k_at(row, piece)) = rk[j];
+                    *(u32x4_t*)(sv + TL::v_at(row, piece)) = rv[j];
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                const uint32_t bits_x = bits;
+                if (x + 1 < i + n) {
+                    const int id_x = id;
+                    if (x + 2 < i + n) id = load_id(x + 2);
+                    bits = load_kv(x + 1, id_x);
+                }
+                if (bits_x) compute(x, bits_x, all_see, odd);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            }
+        }
+
+        // joins the four waves' results and writes them
+        bool whole = true;
+        int slot = 0;
+        if (shared) {
+            const int ra = u - i, rb = ra + R.n;   // the units of (p, h)
+            const bool starts = ra >= first;
+            whole = starts && rb <= u1;
+            slot = 2 * block + (starts ? 1 : 0);
+            if (starts && tid == 0) W.rec[p * hkv + h] = int2{block, (int)((rb * wgs - 1) / total)};
+        }
         l += __shfl_xor(l, 16, 64);
         l += __shfl_xor(l, 32, 64);
-        if (lane < 16) {
-            sM[wave][lane] = m;
-            sL[wave][lane] = l;
-        }
         float* so = (float*)sk;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        float* stat = so + 16 * OP;   // 16 largest scores, 16 sums
+        if (lane < 16) {
+            stat[lane] = m;
+            stat[16 + lane] = l;
+        }
 #pragma unroll
         for (int t = 0; t < D / 16; ++t)
             *(float4*)(so + l16 * OP + t * 16 + g4 * 4) = float4{acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
         __syncthreads();
-        constexpr int N = D / 16;   // elements per thread, of column tid / 16
-        const int col = tid >> 4, d = (tid & 15) * N;
-        float M = sM[0][col], f[4], sum = 0.f, v[N];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) M = fmaxf(M, sM[w][col]);
-        const float Mc = M == -__builtin_inff() ? 0.f : M * c;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            f[w] = exp2_fast(sM[w][col] * c - Mc);
-            sum += f[w] * sL[w][col];
-        }
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            float4 x{0.f, 0.f, 0.f, 0.f};
+        {
+            constexpr int N = D / 16;   // elements per thread, of column tid / 16
+            constexpr int WF = WB / 4;  // floats of a wave's stage
+            const int col = tid >> 4, d = (tid & 15) * N;
+            const float* all = (const float*)stage;
+            float mw[4], M = -kInf, sum = 0.f, v[N];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const float4 y = *(const float4*)((const float*)(stage + w * WB) + col * OP + d + e);
-                x.x += f[w] * y.x;
-                x.y += f[w] * y.y;
-                x.z += f[w] * y.z;
-                x.w += f[w] * y.w;
+                mw[w] = all[w * WF + 16 * OP + col];
+                M = fmaxf(M, mw[w]);
             }
-            v[e] = x.x;
-            v[e + 1] = x.y;
-            v[e + 2] = x.z;
-            v[e + 3] = x.w;
-        }
-        if (!whole) {
-            put_raw<N>(W.few_o + ((int64_t)slot * 16 + col) * D + d, v);
-            if ((tid & 15) == 0) W.few_ml[slot * 16 + col] = float2{M, sum};
-        } else if (col < X.P.nr * a.share) {
-            const int j = col / a.share;
-            const int row = X.P.r0 + j, head = X.h * a.share + (col - j * a.share);
-            const int64_t rh = (int64_t)row * a.n_q_heads + head;
-            if (a.join) {
-                put_raw<N>(W.row_o + rh * D + d, v);
-                if ((tid & 15) == 0) W.row_ml[rh] = float2{M, sum};
-            } else {
-                put_out<N>(a, row, head, D, d, v, sum);
-                if (a.lse && (tid & 15) == 0) a.lse[rh] = lse_of(a, M, sum);
+            const float Mc = M == -kInf ? 0.f : M * c;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                mw[w] = exp2_fast(mw[w] * c - Mc);
+                sum += mw[w] * all[w * WF + 16 * OP + 16 + col];
             }
-        }
-        __syncthreads();
-    };
-    auto clear = [&]() __attribute__((always_inline)) {
-        m = -__builtin_inff();
-        l = 0.f;
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    };
-    if (!SHARED && u1 == 0) {   // rows that see no key
-        clear();
-        finish(L, true, 0);
-        return;
-    }
-
-    int col_pos = -1;   // position of this lane's column, -1: no column
-    auto begin = [&](const At& X) __attribute__((always_inline)) {
-        const int j = l16 / a.share;
-        const bool there = l16 < X.P.nr * a.share;
-        const T* q = (const T*)a.q + (int64_t)(X.P.r0 + j) * a.ldq + (int64_t)(X.h * a.share + l16 - j * a.share) * D;
+            for (int e = 0; e < N; e += 4) {
+                float4 x{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < D / 32; ++s) qf[s] = there ? O::load(q + s * 32 + g4 * 8) : O::zero();
-        if (KIND == 0) col_pos = there ? X.P.pos0 + j : -1;
-        else if (a.window > 0) col_pos = there ? row_position(a, X.P.r0 + j) : -1;
-        else col_pos = there ? X.P.pos1 : -1;
-        clear();
-    };
-    // page number of key `lane` of the wave's unit (lanes 0 .. 31), -1: none
-    auto load_id = [&](const At& X) __attribute__((always_inline)) {
-        const int key = X.R.tile(X.i) * ATTN_FEW_KEYS + wave * KW + lane;
-        return lane < KW && key < X.P.len ? X.P.tbl[key >> a.C.page_shift] : -1;
-    };
-    uint4 rk[NL], rv[NL];
-    // requests the wave's pieces of unit X; the answer's bit k says whether
-    // any column sees key k (the others are read from page 0 and not used)
-    auto load_kv = [&](const At& X, int id) __attribute__((always_inline)) {
-        const int base = X.R.tile(X.i) * ATTN_FEW_KEYS + wave * KW;
-        const int key = base + lane, at = X.P.key0 + key;
-        const bool page_ok = id >= 0 && id < a.C.n_pages;
-        bool seen = lane < KW && key < X.P.len && at <= X.P.pos1;
-        if (a.window > 0) seen = seen && (at > X.P.pos0 - a.window || at < a.n_sink);
-        if (seen && !page_ok && a.status) flag_bad_id(a.status);
-        seen = seen && page_ok;
-        const uint32_t bits = (uint32_t)__ballot(seen);
-        const int page = page_ok ? id : 0;
-        const int mask = (1 << a.C.page_shift) - 1;
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int row = j * RPL + lane / TL::LPR;
-            const int64_t off = (int64_t)__shfl(page, row, 64) * a.C.page_stride +
-                                (int64_t)((base + row) & mask) * a.C.token_stride + (int64_t)X.h * a.C.head_stride +
-                                (lane % TL::LPR) * (16 / (int)sizeof(T));
-            rk[j] = *(const uint4*)((const T*)a.C.k + off);
-            rv[j] = *(const uint4*)((const T*)a.C.v + off);
-        }
-        return bits;
-    };
-    auto store_kv = [&](uint32_t bits) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int row = j * RPL + lane / TL::LPR, piece = lane % TL::LPR;
-            *(uint4*)(sk + TL::k_at(row, piece)) = rk[j];
-            if (bits != 0xffffffffu && !((bits >> row) & 1)) rv[j] = uint4{0u, 0u, 0u, 0u};
-            *(uint4*)(sv + TL::v_at(row, piece)) = rv[j];
-        }
-    };
-    auto compute = [&](const At& X, uint32_t bits) __attribute__((always_inline)) {
-        f32x4_t s[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks) {
-            s[0] = O::mma16(TL::k_frag(sk, l16, ks * 32 + g4 * 8), qf[ks], s[0]);
-            s[1] = O::mma16(TL::k_frag(sk, 16 + l16, ks * 32 + g4 * 8), qf[ks], s[1]);
-        }
-        // element r of s[t]: key 16 t + 4 g4 + r, this lane's column
-        const int lo = X.P.key0 + X.R.tile(X.i) * ATTN_FEW_KEYS + wave * KW;
-        const bool all_see = lo + KW - 1 <= X.P.pos0 && (a.window == 0 || lo > X.P.pos1 - a.window);
-        const bool masked = bits != 0xffffffffu || !all_see;
-        auto sees = [&](int k) __attribute__((always_inline)) {
-            const int at = lo + k;
-            return ((bits >> k) & 1) && at <= col_pos && (a.window == 0 || at > col_pos - a.window || at < a.n_sink);
-        };
-        if (masked) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (!sees(16 * t + 4 * g4 + r)) s[t][r] = -__builtin_inff();
-        }
-        float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                          fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m_new = fmaxf(m, top);
-        const float mc = m_new == -__builtin_inff() ? 0.f : m_new * c;
-        if (__ballot(m_new != m)) {
-            const float f = exp2_fast(m * c - mc);
-            l *= f;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) acc[t] *= f;
-            m = m_new;
-        }
-        f32x8_t p;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            p[r] = exp2_fast(s[0][r] * c - mc);
-            p[4 + r] = exp2_fast(s[1][r] * c - mc);
-        }
-        l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        const typename O::frag pf = O::round(p);
-        // A key that some rows see and others do not may hold infinities or
-        // NaN: 0 times those must not reach the rows that do not see it.
-        const bool mixed = !all_see && X.P.nr > 1;
-        bool odd = false;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-            typename O::frag vf = TL::v_frag(sv, 4 * g4, 16 + 4 * g4, t * 16, l16);
-            if (mixed) odd |= O::clean(vf);
-            acc[t] = O::mma16(vf, pf, acc[t]);
-        }
-        if (mixed && __ballot(odd)) {
-            for (int k = 0; k < KW; ++k) {
-                const int r = k & 3, t = k >> 4;
-                float w = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e == t * 4 + r) w = p[e];
-                w = __shfl(w, ((k >> 2) & 3) * 16 + l16, 64);
-                if (!sees(k)) continue;
-#pragma unroll
-                for (int q = 0; q < D / 16; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x = TL::v_one(sv, k, q * 16 + g4 * 4 + e);
-                        if (non_finite(x)) acc[q][e] += w * x;
-                    }
+                for (int w = 0; w < 4; ++w) {
+                    const float4 y = *(const float4*)(all + w * WF + col * OP + d + e);
+                    x.x += mw[w] * y.x;
+                    x.y += mw[w] * y.y;
+                    x.z += mw[w] * y.z;
+                    x.w += mw[w] * y.w;
+                }
+                v[e] = x.x;
+                v[e + 1] = x.y;
+                v[e + 2] = x.z;
+                v[e + 3] = x.w;
             }
-        }
-    };
-    auto step = [&](At& X) __attribute__((always_inline)) {
-        if (++X.i < X.R.n) return;
-        X.i = 0;
-        if (++X.h < hkv) return;
-        X.h = 0;
-        do {   // in bounds: called only while units remain
-            X.P = load_prob<KIND>(a, ++X.p);
-            X.R = range_of(X.P);
-        } while (X.R.n == 0 && X.p + 1 < n_prob);
-    };
-
-    // C: the unit worked on, L: the unit whose pieces are requested, N: the
-    // one whose page numbers are
-    const int first = u;
-    At C = L;
-    uint32_t bits = load_kv(L, load_id(L));
-    int id = -1;
-    if (u + 1 < u1) {
-        step(L);
-        id = load_id(L);
-    }
-    begin(C);
-    while (true) {
-        store_kv(bits);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const uint32_t bits_c = bits;
-        At N = L;
-        if (u + 1 < u1) {
-            bits = load_kv(L, id);
-            if (u + 2 < u1) {
-                step(N);
-                id = load_id(N);
-            }
-        }
-        if (bits_c) compute(C, bits_c);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const bool last = u + 1 == u1;
-        if (last || C.i + 1 == C.R.n) {
-            bool whole = true;
-            int slot = 0;
-            if (SHARED) {
-                const int ra = u - C.i, rb = ra + C.R.n;   // the units of (p, h)
-                const bool starts = ra >= first;
-                whole = starts && rb <= u1;
-                slot = 2 * blockIdx.x + (starts ? 1 : 0);
-                if (starts && tid == 0) {
-                    const int b1 = (int)((rb * wgs - 1) / total);
-                    W.rec[C.p * hkv + C.h] = int2{(int)blockIdx.x, b1};
+            if (!whole) {
+                put_raw<N>(W.few_o + ((int64_t)slot * 16 + col) * D + d, v);
+                if ((tid & 15) == 0) W.few_ml[slot * 16 + col] = float2{M, sum};
+            } else if (col < P.nr * a.share) {
+                const int j = col / a.share;
+                const int row = P.r0 + j, head = h * a.share + (col - j * a.share);
+                const int64_t rh = (int64_t)row * a.n_q_heads + head;
+                if (a.join) {
+                    put_raw<N>(W.row_o + rh * D + d, v);
+                    if ((tid & 15) == 0) W.row_ml[rh] = float2{M, sum};
+                } else {
+                    put_out<N>(a, row, head, D, d, v, sum);
+                    if (a.lse && (tid & 15) == 0) a.lse[rh] = lse_of(a, M, sum);
                 }
             }
-            finish(C, whole, slot);
-            if (last) break;
-            begin(L);
         }
-        C = L;
-        L = N;
-        ++u;
+        u += n;
+        if (u >= u1) break;
+        __syncthreads();
+        i = 0;
+        if (++h == hkv) {
+            h = 0;
+            do {   // in bounds: units remain
+                P = load_prob(a, kind, ++p);
+                R = range_of(P);
+            } while (R.n == 0 && p + 1 < n_prob);
+        }
     }
 }
 
@@ -688,45 +750,46 @@ void k_attn_few(AttnArgs a) {
 // (problem, column tile, key head, run of key tiles) are numbered with the
 // key head fastest, so that the columns of one head meet in one XCD's L2, and
 // later column tiles (more keys under the causal mask) first.
-template <typename T, int D, int KIND>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) * D <= 256 ? 2 : 1)))
-void k_attn_tile(AttnArgs a) {
+template <typename T, int D, bool PAGED>
+__device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block, uint8_t* stage, int* sh) {
     using TL = Tile<T, D>;
     using O = Op<T>;
     constexpr int KB = ATTN_TILE_KEYS, TC = ATTN_TILE_COLS;
     constexpr int NL = KB * TL::LPR / 256;     // pieces per thread, of K and of V
     constexpr int RPL = 256 / TL::LPR;         // rows one load of the workgroup covers
     constexpr int TB = KB * TL::RB;            // bytes of a staged tile
-    __shared__ __attribute__((aligned(16))) uint8_t stage[2][2][TB];
-    __shared__ int sh[8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l32 = lane & 31, h2 = lane >> 5, l16 = lane & 15, d16 = (lane >> 4) & 1;
     const int hkv = a.C.n_kv_heads;
-    const AttnPart& W = a.part[KIND];
-    const int n_prob = KIND == 0 ? a.B.n_seqs : a.B.n_groups;
+    const AttnPart& W = a.part[kind];
+    const int n_prob = problems(a, kind);
     const float c = a.scale * kLog2e;
     const float kInf = __builtin_inff();
+    const float slack = kSlack / c;
+    int vb[D / 32];   // this lane's place in the stage of values, per 32 dimensions
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) vb[t] = TL::v_base(4 * h2, t * 32 + d16 * 16, l16);
 
-    auto splits_of = [&](const Prob& P, int& nct) __attribute__((always_inline)) {
-        const int64_t cols = (int64_t)P.nr * a.share;
+    auto splits_of = [&](const Prob& Q, int& nct) __attribute__((always_inline)) {
+        const int64_t cols = (int64_t)Q.nr * a.share;
         nct = cols > ATTN_FEW_COLS ? (int)((cols + TC - 1) / TC) : 0;
-        const int n = key_tiles<KB>(a, P, P.pos0, P.pos1).n;
+        const int n = key_tiles<KB>(a, Q, Q.pos0, Q.pos1).n;
         return n > W.spl ? (n + W.spl - 1) / W.spl : 1;
     };
     int p, base;
-    if (!locate(n_prob, blockIdx.x,
+    if (!locate(n_prob, block,
                 [&](int q) {
                     int nct;
-                    const int ns = splits_of(load_prob<KIND>(a, q), nct);
+                    const int ns = splits_of(load_prob(a, kind, q), nct);
                     return nct * ns * hkv;
                 },
                 tid, sh, p, base))
         return;
-    const Prob P = load_prob<KIND>(a, p);
+    const Prob P = load_prob(a, kind, p);
     int nct;
     const int nsplit = splits_of(P, nct);
-    int rem = blockIdx.x - base;
+    int rem = block - base;
     const int h = rem % hkv;
     rem /= hkv;
     const int split = rem / nct;
@@ -735,7 +798,7 @@ void k_attn_tile(AttnArgs a) {
 
     // the workgroup's rows, its key tiles and this split's run of them
     const int j_lo = ct * TC / a.share, j_hi = min(P.nr - 1, (ct * TC + TC - 1) / a.share);
-    const int wg_lo = KIND == 0 ? P.pos0 + j_lo : P.pos0, wg_hi = KIND == 0 ? P.pos0 + j_hi : P.pos1;
+    const int wg_lo = kind == 0 ? P.pos0 + j_lo : P.pos0, wg_hi = kind == 0 ? P.pos0 + j_hi : P.pos1;
     const Range R = key_tiles<KB>(a, P, wg_lo, wg_hi);
     const int i0 = split * W.spl, i1 = min(R.n, i0 + W.spl);
     if (split > 0 && i0 >= R.n) return;
@@ -748,10 +811,10 @@ void k_attn_tile(AttnArgs a) {
     const int row = P.r0 + j, head = h * a.share + (there ? col - j * a.share : 0);
     const bool wave_there = ct * TC + wave * 32 < n_cols;
     int col_pos = -1;
-    if (there) col_pos = KIND == 0 ? P.pos0 + j : a.window > 0 ? row_position(a, row) : P.pos1;
+    if (there) col_pos = kind == 0 ? P.pos0 + j : a.window > 0 ? row_position(a, row) : P.pos1;
     // least and largest position of the wave's columns
-    const int wv_lo = KIND == 0 ? P.pos0 + (ct * TC + wave * 32) / a.share : P.pos0;
-    const int wv_hi = KIND == 0 ? min(P.pos1, P.pos0 + (ct * TC + wave * 32 + 31) / a.share) : P.pos1;
+    const int wv_lo = kind == 0 ? P.pos0 + (ct * TC + wave * 32) / a.share : P.pos0;
+    const int wv_hi = kind == 0 ? min(P.pos1, P.pos0 + (ct * TC + wave * 32 + 31) / a.share) : P.pos1;
 
     typename O::frag qf[D / 16];
     {
@@ -771,7 +834,7 @@ void k_attn_tile(AttnArgs a) {
         const int key = R.tile(i) * KB + lane;
         return key < P.len ? P.tbl[key >> a.C.page_shift] : -1;
     };
-    uint4 rk[NL], rv[NL];
+    u32x4_t rk[NL], rv[NL];
     auto load_kv = [&](int i, int id) __attribute__((always_inline)) {
         const int base_k = R.tile(i) * KB;
         const int key = base_k + lane, at = P.key0 + key;
@@ -779,30 +842,11 @@ void k_attn_tile(AttnArgs a) {
         bool seen = key < P.len && at <= wg_hi;
         if (a.window > 0) seen = seen && (at > wg_lo - a.window || at < a.n_sink);
         if (seen && !page_ok && a.status) flag_bad_id(a.status);
-        seen = seen && page_ok;
-        const uint64_t bits = __ballot(seen);
-        const int page = page_ok ? id : 0;
-        const int mask = (1 << a.C.page_shift) - 1;
-#pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int r = n * RPL + tid / TL::LPR;
-            const int64_t off = (int64_t)__shfl(page, r, 64) * a.C.page_stride +
-                                (int64_t)((base_k + r) & mask) * a.C.token_stride + (int64_t)h * a.C.head_stride +
-                                (tid % TL::LPR) * (16 / (int)sizeof(T));
-            rk[n] = *(const uint4*)((const T*)a.C.k + off);
-            rv[n] = *(const uint4*)((const T*)a.C.v + off);
-        }
-        return bits;
+        request<T, D, NL, RPL, PAGED, false>(a, page_ok ? id : 0, base_k, wave * (64 / TL::LPR), h, lane, rk, rv);
+        return (uint64_t)__ballot(seen && page_ok);
     };
-    auto store_kv = [&](int buf, uint64_t bits) __attribute__((always_inline)) {
-#pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const int r = n * RPL + tid / TL::LPR, piece = tid % TL::LPR;
-            *(uint4*)(stage[buf][0] + TL::k_at(r, piece)) = rk[n];
-            if (bits != ~0ull && !((bits >> r) & 1)) rv[n] = uint4{0u, 0u, 0u, 0u};
-            *(uint4*)(stage[buf][1] + TL::v_at(r, piece)) = rv[n];
-        }
-    };
+    // sh[6 + buffer]: some value of a tile that columns see in part is not finite
+    if (tid == 0) sh[6] = sh[7] = 0;
 
     uint64_t bits = 0;
     int id = -1;
@@ -810,54 +854,80 @@ void k_attn_tile(AttnArgs a) {
         bits = load_kv(i0, load_id(i0));
         if (i0 + 1 < i1) id = load_id(i0 + 1);
     }
+    __syncthreads();
     for (int i = i0; i < i1; ++i) {
         const int buf = (i - i0) & 1;
-        store_kv(buf, bits);
-        __syncthreads();
-        const uint64_t bits_c = bits;
-        if (i + 1 < i1) {
-            bits = load_kv(i + 1, id);
-            if (i + 2 < i1) id = load_id(i + 2);
-        }
+        uint8_t* sk = stage + buf * 2 * TB;
+        uint8_t* sv = sk + TB;
         const int lo = P.key0 + R.tile(i) * KB;
+        const int r0 = tid / TL::LPR, piece = tid % TL::LPR;
+        if (bits != ~0ull) hide_rows<NL>(rv, bits, r0, RPL);
+        const bool wg_all = bits == ~0ull && lo + KB - 1 <= wg_lo && (a.window == 0 || lo > wg_hi - a.window);
+        if (!wg_all) {
+            bool odd = false;
+#pragma unroll
+            for (int n = 0; n < NL; ++n) odd |= odd_piece<T>(rv[n]);
+            if (__ballot(odd) && lane == 0) sh[6 + buf] = 1;
+        }
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            *(u32x4_t*)(sk + TL::k_at(n * RPL + r0, piece)) = rk[n];
+            *(u32x4_t*)(sv + TL::v_at(n * RPL + r0, piece)) = rv[n];
+        }
+        __syncthreads();
+        const uint64_t bits_i = bits;
+        if (i + 1 < i1) {
+            const int id_i = id;
+            if (i + 2 < i1) id = load_id(i + 2);
+            bits = load_kv(i + 1, id_i);
+        }
         if (!wave_there || lo > wv_hi) continue;
-        const uint8_t* sk = stage[buf][0];
-        const uint8_t* sv = stage[buf][1];
+        const bool all_see = bits_i == ~0ull && lo + KB - 1 <= wv_lo && (a.window == 0 || lo > wv_hi - a.window);
+        const bool odd = !wg_all && *(volatile int*)(sh + 6 + buf) != 0;
         // element r of s[kb]: key 32 kb + 8 (r / 4) + 4 h2 + r % 4
         f32x16_t s[2];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        for (int r = 0; r < 16; ++r) s[0][r] = s[1][r] = 0.f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[kb][r] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                s[kb] = O::mma32(TL::k_frag(sk, kb * 32 + l32, ks * 16 + h2 * 8), qf[ks], s[kb]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+            s[0] = O::mma32(TL::k_frag(sk, l32, ks * 16 + h2 * 8), qf[ks], s[0]);
+            s[1] = O::mma32(TL::k_frag(sk + 32 * TL::RB, l32, ks * 16 + h2 * 8), qf[ks], s[1]);
         }
-        const bool all_see = lo + KB - 1 <= wv_lo && (a.window == 0 || lo > wv_hi - a.window);
-        auto sees = [&](int k) __attribute__((always_inline)) {
-            const int at = lo + k;
-            return ((bits_c >> k) & 1) && at <= col_pos && (a.window == 0 || at > col_pos - a.window || at < a.n_sink);
-        };
-        if (bits_c != ~0ull || !all_see) {
+        if constexpr (sizeof(T) == 2) {
+            // K's operands are requested four products ahead of their use
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+            for (int n = 0; n < D / 16 - 2; ++n) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        }
+        if (!all_see) {
+            asm volatile("");   // a branch: most tiles need no mask
+            const Sees S(a, col_pos, lo + 4 * h2);
+            const uint64_t mine = bits_i >> (4 * h2);
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (!sees(32 * kb + 8 * (r >> 2) + 4 * h2 + (r & 3))) s[kb][r] = -kInf;
+                for (int r = 0; r < 16; ++r) {
+                    const int k = 32 * kb + 8 * (r >> 2) + (r & 3);
+                    s[kb][r] = S.at(k) & ((uint32_t)(mine >> k) & 1u) ? s[kb][r] : -kInf;
+                }
         }
-        float top = s[0][0];
+        float top = max_of(s[0][0], s[1][0]);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, fmaxf(s[0][r], s[1][r]));
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, max_of(s[0][r], s[1][r]));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m_new = fmaxf(m, top);
-        const float mc = m_new == -kInf ? 0.f : m_new * c;
-        if (__ballot(m_new != m)) {
-            const float f = exp2_fast(m * c - mc);
+        if (__ballot(top > m + slack)) {
+            const bool up = top > m + slack;   // a column's own matter: its neighbours do not change its bits
+            const float f = up ? exp2_fast((m - top) * c) : 1.f;   // from -infinity: 0
             l *= f;
 #pragma unroll
             for (int t = 0; t < D / 32; ++t) acc[t] *= f;
-            m = m_new;
+            if (up) m = top;
         }
+        const float mc = m == -kInf ? 0.f : m * c;
         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
@@ -877,50 +947,58 @@ void k_attn_tile(AttnArgs a) {
                 for (int e = 0; e < 8; ++e) x[e] = s[kb][8 * t + e];
                 pf[kb][t] = O::round(x);
             }
-        const int k4 = 4 * h2;
-        if (all_see) {
+        // the four 16-key steps of the second product
+        auto each_step = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t)
+            for (int t = 0; t < D / 32; ++t) f(TL::template v_frag<0, 8>(sv + vb[t]), pf[0][0], t);
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+            for (int t = 0; t < D / 32; ++t) f(TL::template v_frag<16, 24>(sv + vb[t]), pf[0][1], t);
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        acc[t] = O::mma32(TL::v_frag(sv, kb * 32 + x * 16 + k4, kb * 32 + x * 16 + 8 + k4,
-                                                     t * 32 + d16 * 16, l16),
-                                          pf[kb][x], acc[t]);
-        } else {
-            // a key that some columns see and others do not may hold
-            // infinities or NaN: 0 times those must not reach the others
-            bool odd = false;
+            for (int t = 0; t < D / 32; ++t) f(TL::template v_frag<32, 40>(sv + vb[t]), pf[1][0], t);
 #pragma unroll
-            for (int t = 0; t < D / 32; ++t)
+            for (int t = 0; t < D / 32; ++t) f(TL::template v_frag<48, 56>(sv + vb[t]), pf[1][1], t);
+        };
+        if (!odd) {
+            each_step([&](const typename O::frag& vf, const typename O::frag& w, int t)
+                          __attribute__((always_inline)) { acc[t] = O::mma32(vf, w, acc[t]); });
+            if constexpr (sizeof(T) == 2) {
+                // V's operands are requested four products ahead of their use
+                constexpr int NM = 4 * (D / 32);
+                __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        typename O::frag vf = TL::v_frag(sv, kb * 32 + x * 16 + k4, kb * 32 + x * 16 + 8 + k4,
-                                                         t * 32 + d16 * 16, l16);
-                        odd |= O::clean(vf);
-                        acc[t] = O::mma32(vf, pf[kb][x], acc[t]);
-                    }
-            if (__ballot(odd)) {
-                for (int k = 0; k < KB; ++k) {
-                    const int e = ((k >> 3) & 3) * 4 + (k & 3);
-                    float w = 0.f;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (r == e) w = k < 32 ? s[0][r] : s[1][r];
-                    w = __shfl(w, ((k >> 2) & 1) * 32 + l32, 64);
-                    if (!sees(k)) continue;
-#pragma unroll
-                    for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const float x = TL::v_one(sv, k, t * 32 + 8 * (r >> 2) + k4 + (r & 3));
-                            if (non_finite(x)) acc[t][r] += w * x;
-                        }
+                for (int n = 0; n < NM - 4; ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
                 }
+                __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
             }
+            continue;
+        }
+        asm volatile("");
+        // Infinities or NaN among values that some columns do not see: they
+        // are left out of the product (0 times them is NaN) and added to the
+        // columns that see them.
+        each_step([&](typename O::frag vf, const typename O::frag& w, int t) __attribute__((always_inline)) {
+            O::clean(vf);
+            acc[t] = O::mma32(vf, w, acc[t]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        const Sees S(a, col_pos, lo);
+        for (int k = 0; k < KB; ++k) {
+            const int e = ((k >> 3) & 3) * 4 + (k & 3);
+            float w = 0.f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (r == e) w = k < 32 ? s[0][r] : s[1][r];
+            w = __shfl(w, ((k >> 2) & 1) * 32 + l32, 64);
+            if (!S.at(k) || !((bits_i >> k) & 1)) continue;
+#pragma unroll
+            for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float x = TL::v_one(sv, k, t * 32 + 8 * (r >> 2) + 4 * h2 + (r & 3));
+                    if (non_finite(x)) acc[t][r] += w * x;
+                }
         }
     }
 
@@ -928,7 +1006,7 @@ void k_attn_tile(AttnArgs a) {
     if (!there) return;
     const bool whole = nsplit == 1;
     const int64_t rh = (int64_t)row * a.n_q_heads + head;
-    const int64_t sc = (int64_t)blockIdx.x * TC + wave * 32 + l32;
+    const int64_t sc = (int64_t)block * TC + wave * 32 + l32;
 #pragma unroll
     for (int t = 0; t < D / 32; ++t)
 #pragma unroll
@@ -946,148 +1024,207 @@ void k_attn_tile(AttnArgs a) {
     }
 }
 
+// Both forms, over own tokens and shared prefixes, in one launch: a
+// workgroup's number says which.  Tiled items come first (the longest ones);
+// the few-column workgroups, bound by memory, run beside and after them.
+template <typename T, int D, bool PAGED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) * D <= 256 ? 2 : 1)))
+void k_attn(AttnArgs a) {
+    // a staged tile pair, twice: two buffers of 64 keys, or four waves' 32 keys
+    __shared__ __attribute__((aligned(16))) uint8_t stage[4 * ATTN_TILE_KEYS * Tile<T, D>::RB];
+    __shared__ int sh[8];
+    int b = blockIdx.x;
+#pragma unroll 1
+    for (int kind = 1; kind >= 0; --kind) {
+        if (b < a.part[kind].tile_grid) {
+            attn_tile<T, D, PAGED>(a, kind, b, stage, sh);
+            return;
+        }
+        b -= a.part[kind].tile_grid;
+    }
+#pragma unroll 1
+    for (int kind = 1; kind >= 0; --kind) {
+        const int n = a.part[kind].few_grid;
+        if (b < n) {
+            attn_few<T, D, PAGED>(a, kind, b, n, stage, sh);
+            return;
+        }
+        b -= n;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Join
 // ---------------------------------------------------------------------------
 
-// A wave per (row, query head): adds the partial results of its own keys and
-// of the shared prefix, each scaled to the largest score of all, in their
-// fixed order.  Reads every partial once.
+// Adds the partial results of a row's own keys and of its shared prefix, each
+// scaled to the largest reference score, in their fixed order.  A wave takes
+// one row and four query heads, 16 lanes each (the row's lookups, a chain of
+// dependent loads, are most of a small join's time and are shared by the
+// four); every partial result is read once.
+//
+// by_row: all rows (a shared prefix, or split tiled items).  Otherwise only
+// rows of few-column sequences can have partial results, and the waves are
+// numbered by (sequence, row in it) so that a prompt's rows cost nothing.
 template <int D>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    constexpr int N = D / 64;
-    const int lane = threadIdx.x & 63;
-    const int64_t rh = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int by_row, int rows_of_few) {
+    constexpr int N = D / 16;   // elements per lane
+    const int lane = threadIdx.x & 63, sub = lane >> 4, sl = lane & 15;
     const KvBatchDev& B = a.B;
-    if (rh >= (int64_t)B.n_rows * a.n_q_heads) return;
-    const int row = (int)(rh / a.n_q_heads), head = (int)(rh - (int64_t)row * a.n_q_heads);
-    const int h = head / a.share, hkv = a.C.n_kv_heads;
-    const int s = wave_find_run(B.row_off, B.n_seqs, row, lane);
-    if (s >= B.n_seqs || row < B.row_off[0]) return;
+    const int blocks = (a.n_q_heads + 3) / 4;   // of four heads
+    const int64_t unit = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t at_row = unit / blocks;
+    const int head = (int)(unit - at_row * blocks) * 4 + sub;
+    int s, row;
+    if (by_row) {
+        if (at_row >= B.n_rows) return;
+        row = (int)at_row;
+        s = wave_find_run(B.row_off, B.n_seqs, row, lane);
+        if (s >= B.n_seqs) return;
+    } else {
+        s = (int)(at_row / rows_of_few);
+        if (s >= B.n_seqs) return;
+        row = -1;
+    }
+    const Prob P = load_prob(a, 0, s);
+    const int j = by_row ? row - P.r0 : (int)(at_row - (int64_t)s * rows_of_few);
+    if (j < 0 || j >= P.nr) return;
+    row = P.r0 + j;
+    const bool few = is_few(a, P);
+    const bool mine = head < a.n_q_heads;
+    const int hd = mine ? head : a.n_q_heads - 1;
+    const int h = hd / a.share, hkv = a.C.n_kv_heads;
+    const int col = j * a.share + (hd - h * a.share);
+    const int64_t rh = (int64_t)row * a.n_q_heads + hd;
+
+    // where problem Q's partial results of column x lie: n of them, the i-th
+    // at places place(i) of o and ml (0: none)
+    struct Parts {
+        const float* o;
+        const float2* ml;
+        int n, first, step;     // places first + i * step, and
+        int other, last;        // the 0-th at `other`; places end at `last`
+    };
+    auto parts_of = [&](int kind, const Prob& Q, int q, int x) __attribute__((always_inline)) {
+        const AttnPart& W = a.part[kind];
+        const Parts one{W.row_o, W.row_ml, a.join ? 1 : 0, (int)rh, 0, (int)rh, (int)rh};
+        Parts r{W.few_o, W.few_ml, 0, 0, 0, 0, 0};
+        if (is_few(a, Q)) {
+            if (W.few == 1) return one;
+            if (key_tiles<ATTN_FEW_KEYS>(a, Q, Q.pos0, Q.pos1).n == 0) return r;
+            const int2 b = W.rec[q * hkv + h];
+            if (b.x == b.y) return one;
+            r.n = min(b.y - b.x + 1, ATTN_FEW_WGS);
+            r.first = 2 * b.x * 16 + x;
+            r.step = 32;
+            r.other = r.first + 16;
+            r.last = 2 * ATTN_FEW_WGS * 16 - 1;
+            return r;
+        }
+        const int4 it = W.slots ? W.item[q] : int4{0, 1, 1, 0};
+        if (it.z == 1) return one;
+        const int ct = x / ATTN_TILE_COLS;
+        const int j_lo = ct * ATTN_TILE_COLS / a.share;
+        const int j_hi = min(Q.nr - 1, (ct * ATTN_TILE_COLS + ATTN_TILE_COLS - 1) / a.share);
+        const int n = key_tiles<ATTN_TILE_KEYS>(a, Q, kind == 0 ? Q.pos0 + j_lo : Q.pos0,
+                                                kind == 0 ? Q.pos0 + j_hi : Q.pos1).n;
+        r.o = W.tile_o;
+        r.ml = W.tile_ml;
+        r.n = min(max(1, (n + W.spl - 1) / W.spl), W.tile_grid);
+        r.first = r.other = (it.x + (it.y - 1 - ct) * hkv + h) * ATTN_TILE_COLS + x % ATTN_TILE_COLS;
+        r.step = it.y * hkv * ATTN_TILE_COLS;
+        r.last = W.tile_grid * ATTN_TILE_COLS - 1;
+        return r;
+    };
+
     const float c = a.scale * kLog2e;
-    float M = -__builtin_inff(), L = 0.f, v[N];
+    const float kInf = __builtin_inff();
+    float M = -kInf, L = 0.f, v[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] = 0.f;
-
-    // adds n partial results, the i-th at o + at(i) * D and ml[at(i)]; `most`
-    // bounds the places, whatever the batch's offsets say
-    auto add = [&](int n, int64_t most, const float* o, const float2* ml, auto place) __attribute__((always_inline)) {
-        auto at = [&](int i) { return max((int64_t)0, min(place(i), most - 1)); };
-        for (int i0 = 0; i0 < n; i0 += 64) {
-            const int here = min(64, n - i0);
-            const float2 x = lane < here ? ml[at(i0 + lane)] : float2{-__builtin_inff(), 0.f};
+    auto add = [&](const Parts& R) __attribute__((always_inline)) {
+        // whatever the batch's offsets say, places stay inside the workspace
+        auto at = [&](int i) { return min(max(i == 0 ? R.other : R.first + i * R.step, 0), R.last); };
+        for (int i0 = 0; __ballot(i0 < R.n); i0 += 16) {
+            const int here = min(16, R.n - i0);
+            const float2 x = sl < here ? R.ml[at(i0 + sl)] : float2{-kInf, 0.f};
             float top = x.x;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
             const float m_new = fmaxf(M, top);
-            const float mc = m_new == -__builtin_inff() ? 0.f : m_new * c;
+            const float mc = m_new == -kInf ? 0.f : m_new * c;
             const float f = exp2_fast(M * c - mc);
-            L *= f;
+            const float w = exp2_fast(x.x * c - mc);
+            float sum = sl < here ? w * x.y : 0.f;
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d, 64);
+            L = L * f + sum;
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] *= f;
             M = m_new;
-            const float w = exp2_fast(x.x * c - mc);
-            float sum = lane < here ? w * x.y : 0.f;
+            for (int i1 = 0; __ballot(i1 < here); i1 += 4) {
+                float4 y[4][N / 4];
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
-            L += sum;
-#pragma unroll 4
-            for (int i = 0; i < here; ++i) {
-                const float wi = __shfl(w, i, 64);
-                const float* src = o + at(i0 + i) * D + lane * N;
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i1 + u < here ? i0 + i1 + u : 0;
+                    const float* src = R.o + (int64_t)at(i) * D + sl * N;
 #pragma unroll
-                for (int e = 0; e < N; ++e) v[e] += wi * src[e];
+                    for (int e = 0; e < N / 4; ++e)
+                        if (i1 + u < here) y[u][e] = *(const float4*)(src + 4 * e);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float wi = __shfl(w, (i1 + u) & 15, 16);
+                    if (i1 + u < here) {
+#pragma unroll
+                        for (int e = 0; e < N / 4; ++e) {
+                            v[4 * e] += wi * y[u][e].x;
+                            v[4 * e + 1] += wi * y[u][e].y;
+                            v[4 * e + 2] += wi * y[u][e].z;
+                            v[4 * e + 3] += wi * y[u][e].w;
+                        }
+                    }
+                }
             }
         }
     };
-    auto add_part = [&](const AttnPart& W, const Prob& P, int p, int col, int pos_lo, int pos_hi) __attribute__((always_inline)) {
-        const bool few = (int64_t)P.nr * a.share <= ATTN_FEW_COLS;
-        if (few) {
-            if (P.len <= 0) return;
-            if (W.few == 1) {
-                add(1, rh + 1, W.row_o, W.row_ml, [&](int) { return rh; });
-                return;
-            }
-            if (key_tiles<ATTN_FEW_KEYS>(a, P, P.pos0, P.pos1).n == 0) return;
-            const int2 b = W.rec[p * hkv + h];
-            if (b.x == b.y) {
-                if (a.join) add(1, rh + 1, W.row_o, W.row_ml, [&](int) { return rh; });
-                return;
-            }
-            add(min(b.y - b.x + 1, ATTN_FEW_WGS), (int64_t)2 * ATTN_FEW_WGS * 16, W.few_o, W.few_ml, [&](int i) {
-                return (int64_t)(i == 0 ? 2 * b.x + 1 : 2 * (b.x + i)) * 16 + col;
-            });
-        } else {
-            const int ct = col / ATTN_TILE_COLS;
-            const int n = key_tiles<ATTN_TILE_KEYS>(a, P, pos_lo, pos_hi).n;
-            const int4 it = W.slots ? W.item[p] : int4{0, 1, 1, 0};
-            if (it.z == 1) {
-                if (a.join) add(1, rh + 1, W.row_o, W.row_ml, [&](int) { return rh; });
-                return;
-            }
-            const int used = max(1, (n + W.spl - 1) / W.spl);
-            add(min(used, W.tile_grid), (int64_t)W.tile_grid * ATTN_TILE_COLS, W.tile_o, W.tile_ml, [&](int i) {
-                return (int64_t)(it.x + (i * it.y + (it.y - 1 - ct)) * hkv + h) * ATTN_TILE_COLS + (col % ATTN_TILE_COLS);
-            });
-        }
-    };
 
-    const Prob P = load_prob<0>(a, s);
-    const int j = row - P.r0;
-    if (j < 0 || j >= P.nr) return;
-    const int col = j * a.share + (head - h * a.share);
-    // without a prefix, whole results are in place already
-    if (!a.join) {
-        const bool few = (int64_t)P.nr * a.share <= ATTN_FEW_COLS;
-        if (few) {
-            if (a.part[0].few == 1) return;
-            if (key_tiles<ATTN_FEW_KEYS>(a, P, P.pos0, P.pos1).n > 0) {
-                const int2 b = a.part[0].rec[s * hkv + h];
-                if (b.x == b.y) return;
-            }
-        } else if (!a.part[0].slots || a.part[0].item[s].z == 1) {
-            return;
+    Parts own = parts_of(0, P, s, col);
+    bool write = mine;
+    if (!a.join) {   // whole results are in place already
+        if (few && a.part[0].few == 1) return;
+        const bool partial = own.n > 0 || (few && key_tiles<ATTN_FEW_KEYS>(a, P, P.pos0, P.pos1).n == 0);
+        write = write && partial;
+        if (!__ballot(write)) return;
+    }
+    if (P.pos0 + j < P.key0) {   // more rows than tokens: this row has no place and sees nothing
+        own.n = 0;
+    } else if (a.join && B.n_groups) {
+        const int g = wave_find_run(B.group_off, B.n_groups, s, lane);
+        if (g < B.n_groups) {
+            const Prob G = load_prob(a, 1, g);
+            const int gj = row - G.r0;
+            if (gj >= 0 && gj < G.nr && G.len > 0) add(parts_of(1, G, g, gj * a.share + (hd - h * a.share)));
         }
     }
-    const bool none = P.pos0 + j < P.key0;   // more rows than tokens: this row has no place
-    if (!none) {
-        const int ct = col / ATTN_TILE_COLS;
-        const int j_lo = ct * ATTN_TILE_COLS / a.share;
-        const int j_hi = min(P.nr - 1, (ct * ATTN_TILE_COLS + ATTN_TILE_COLS - 1) / a.share);
-        if (a.join && B.n_groups) {
-            const int g = wave_find_run(B.group_off, B.n_groups, s, lane);
-            if (g < B.n_groups) {
-                const Prob G = load_prob<1>(a, g);
-                const int gj = row - G.r0;
-                if (gj >= 0 && gj < G.nr)
-                    add_part(a.part[1], G, g, gj * a.share + (head - h * a.share), G.pos0, G.pos1);
-            }
-        }
-        add_part(a.part[0], P, s, col, P.pos0 + j_lo, P.pos0 + j_hi);
-    }
-    put_out<N>(a, row, head, D, lane * N, v, L);
-    if (a.lse && lane == 0) a.lse[rh] = lse_of(a, M, L);
-}
-
-template <typename T, int D, int KIND>
-void launch_kind(const AttnArgs& a, hipStream_t stream) {
-    const AttnPart& W = a.part[KIND];
-    const int n_prob = KIND == 0 ? a.B.n_seqs : a.B.n_groups;
-    if (W.few == 1)
-        hipLaunchKernelGGL((k_attn_few<T, D, KIND, false>), dim3((unsigned)(n_prob * a.C.n_kv_heads)), dim3(256), 0,
-                           stream, a);
-    else if (W.few == 2)
-        hipLaunchKernelGGL((k_attn_few<T, D, KIND, true>), dim3(ATTN_FEW_WGS), dim3(256), 0, stream, a);
-    if (W.tile) hipLaunchKernelGGL((k_attn_tile<T, D, KIND>), dim3((unsigned)W.tile_grid), dim3(256), 0, stream, a);
+    add(own);
+    if (!write) return;
+    put_out<N>(a, row, head, D, sl * N, v, L);
+    if (a.lse && sl == 0) a.lse[rh] = lse_of(a, M, L);
 }
 
 template <typename T, int D>
 hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
-    if (a.join) launch_kind<T, D, 1>(a, stream);
-    launch_kind<T, D, 0>(a, stream);
+    const int64_t grid = (int64_t)a.part[0].tile_grid + a.part[1].tile_grid + a.part[0].few_grid + a.part[1].few_grid;
+    const bool paged = (1 << a.C.page_shift) >= 64 / Tile<T, D>::LPR;
+    if (paged) hipLaunchKernelGGL((k_attn<T, D, true>), dim3((unsigned)grid), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((k_attn<T, D, false>), dim3((unsigned)grid), dim3(256), 0, stream, a);
     if (a.need_join) {
-        const int64_t waves = (int64_t)a.B.n_rows * a.n_q_heads;
-        hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)ceil_div(waves, 4)), dim3(256), 0, stream, a);
+        const int by_row = a.join || a.part[0].slots;
+        const int few_rows = std::max(1, std::min(ATTN_FEW_COLS / a.share, a.part[0].max_rows));
+        const int64_t rows = by_row ? a.B.n_rows : (int64_t)a.B.n_seqs * few_rows;
+        hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)ceil_div(rows * ceil_div(a.n_q_heads, 4), 4)), dim3(256), 0,
+                           stream, a, by_row, few_rows);
     }
     return hipGetLastError();
 }
@@ -1121,6 +1258,7 @@ void plan_attn(AttnPlan& P, int32_t head_dim, const int32_t (&n_prob)[2], const 
         if (a.share <= ATTN_FEW_COLS) {
             const int64_t units = ceil_div(reach, ATTN_FEW_KEYS);
             W.few = units <= 2 ? 1 : 2;
+            W.few_grid = W.few == 1 ? n_prob[k] * hkv : ATTN_FEW_WGS;
             if (W.few == 2) a.need_join = 1;
             if (ceil_div(max_len[k], ATTN_FEW_KEYS) > 2) {
                 P.off[k][0] = take((size_t)n_prob[k] * hkv * sizeof(int2));
@@ -1129,7 +1267,6 @@ void plan_attn(AttnPlan& P, int32_t head_dim, const int32_t (&n_prob)[2], const 
             }
         }
         if ((int64_t)max_rows[k] * a.share > ATTN_FEW_COLS) {
-            W.tile = 1;
             const int64_t nct = (int64_t)a.B.n_rows * a.share / ATTN_TILE_COLS + std::min(n_prob[k], a.B.n_rows);
             const int64_t tiles = ceil_div(reach, ATTN_TILE_KEYS) + 1;
             const int64_t spl = std::max<int64_t>(8, ceil_div(tiles * nct * hkv, 1024));

@@ -33,6 +33,7 @@ lora_status_t check_cache(const lora_kv_cache_t* c, KvDev& C) {
     if (!al16(c->k) || !al16(c->v) || !ld16(c->page_stride, eb) || !ld16(c->token_stride, eb) ||
         !ld16(c->head_stride, eb))
         return LORA_E_UNSUPPORTED;
+    if (c->token_stride * c->page_size >= kMost) return LORA_E_UNSUPPORTED;   // offsets in a page are 32-bit
     C.k = c->k;
     C.v = c->v;
     C.page_stride = c->page_stride;

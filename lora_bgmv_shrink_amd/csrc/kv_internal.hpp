@@ -83,9 +83,9 @@ struct AttnPart {       // one kind's kernels and where their partial results li
     int32_t max_rows;   // host bounds that the sizes below rest on: a problem's rows
     int32_t max_len;    // and keys past them are not looked at
     int32_t few;        // 0: not launched, 1: a workgroup per (problem, head), 2: units shared
-    int32_t tile;       // launched
+    int32_t few_grid;   // its workgroups
     int32_t spl;        // key tiles of a tiled item
-    int32_t tile_grid;  // tiled items at most
+    int32_t tile_grid;  // tiled items at most (0: no problem has that many columns)
     int32_t slots;      // tiled items write partial results (some problem may be split)
     int2* rec;          // few 2: first and last workgroup of each (problem, head)
     float* few_o;       // [2 * ATTN_FEW_WGS][16][head_dim], unnormalised
