@@ -76,7 +76,6 @@ hipError_t launch_kv_append(const AppendArgs& a, lora_dtype_t in, lora_dtype_t c
 constexpr int ATTN_FEW_COLS = 16;
 constexpr int ATTN_FEW_KEYS = 128;     // keys of a few-column work unit
 constexpr int ATTN_FEW_WGS = 512;      // workgroups that share the units
-constexpr int ATTN_TILE_COLS = 128;
 constexpr int ATTN_TILE_KEYS = 64;
 
 struct AttnPart {       // one kind's kernels and where their partial results lie
@@ -91,7 +90,7 @@ struct AttnPart {       // one kind's kernels and where their partial results li
     float* few_o;       // [2 * ATTN_FEW_WGS][16][head_dim], unnormalised
     float2* few_ml;     // [..][16] (largest score, sum)
     int4* item;         // tiled: first item, column tiles, splits of each problem
-    float* tile_o;      // [tile_grid][ATTN_TILE_COLS][head_dim]
+    float* tile_o;      // [tile_grid][tile_cols][head_dim]
     float2* tile_ml;
     float* row_o;       // [n_rows][n_q_heads][head_dim]: whole results that the join still needs
     float2* row_ml;
@@ -112,6 +111,8 @@ struct AttnArgs {
     int32_t* status;            // may be null
     int32_t join;               // outputs come from the join launch alone
     int32_t need_join;
+    int32_t tile_cols;          // columns of a tiled item: 128 or 256
+    int32_t together;           // both forms in one launch
     AttnPart part[2];
 };
 struct AttnPlan {
