@@ -942,6 +942,8 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
 // (problem, column tile, key head, run of key tiles) are numbered with the
 // key head fastest, so that the columns of one head meet in one XCD's L2, and
 // later column tiles (more keys under the causal mask) first.
+// Rows of up to 256 bytes leave the registers for tiles of 256 columns.
+template <typename T, int D> constexpr bool kWide = sizeof(T) * D <= 256;
 template <typename T, int D, bool PAGED, int NW>
 __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block, uint8_t* stage, int* sh) {
     using TL = Tile<T, D>;
@@ -1015,13 +1017,13 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
     const int row = P.r0 + j, head = h * a.share + (there ? col - j * a.share : 0);
     int col_pos = -1;
     if (there) col_pos = kind == 0 ? lowest(P, j) : P.pos1;
-    if (kind == 1 && there && (a.window > 0 || !a.together)) {
+    if (kind == 1 && there && (a.window > 0 || !a.decode)) {
         int seq_rows;
         const int at = row_position(a, row, seq_rows);
         if (a.window > 0) col_pos = at;
         there = (int64_t)seq_rows * a.share <= ATTN_FEW_COLS;   // the others walk the prefix themselves
     }
-    if (kind == 1 && !a.together && !__syncthreads_or(there)) return;
+    if (kind == 1 && !a.decode && !__syncthreads_or(there)) return;
     const bool wave_there = __ballot(there) != 0;
     // least and largest position of the wave's columns
     const int wv_lo = kind == 0 ? lowest(P, (ct * TC + wave * 32) / a.share) : P.pos0;
@@ -1296,10 +1298,10 @@ void k_attn_tile(AttnArgs a) {
     const int kind = b < n1 ? 1 : 0;
     attn_tile<T, D, PAGED, NW>(a, kind, kind ? b : b - n1, stage, sh);
 }
-// Decode rows behind shared prefixes: the tiled form over the prefixes, bound
-// by the matrix cores, and the few-column form over the rows' own tokens,
-// bound by memory, side by side: their workgroups alternate, eight by eight
-// so that each kind still goes round the XCDs.
+// Both forms in one launch, side by side (decode rows behind a shared prefix:
+// the tiled form over the prefix, the few-column form over the rows' own
+// tokens): their workgroups alternate, eight by eight so that each kind still
+// goes round the XCDs.
 template <typename T, int D, bool PAGED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) * D <= 256 ? 2 : 1)))
 void k_attn_both(AttnArgs a) {
@@ -1499,10 +1501,13 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
     }
     if (tiles && !a.together) {
         const dim3 grid(tiles), block(2 * a.tile_cols);
-        if (a.tile_cols == 256) {
-            if (paged) hipLaunchKernelGGL((k_attn_tile<T, D, true, 8>), grid, block, 0, stream, a);
-            else hipLaunchKernelGGL((k_attn_tile<T, D, false, 8>), grid, block, 0, stream, a);
-        } else {
+        bool wide = false;
+        if constexpr (kWide<T, D>) {
+            wide = a.tile_cols == 256;
+            if (wide && paged) hipLaunchKernelGGL((k_attn_tile<T, D, true, 8>), grid, block, 0, stream, a);
+            else if (wide) hipLaunchKernelGGL((k_attn_tile<T, D, false, 8>), grid, block, 0, stream, a);
+        }
+        if (!wide) {
             if (paged) hipLaunchKernelGGL((k_attn_tile<T, D, true, 4>), grid, block, 0, stream, a);
             else hipLaunchKernelGGL((k_attn_tile<T, D, false, 4>), grid, block, 0, stream, a);
         }
@@ -1523,7 +1528,7 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-void plan_attn(AttnPlan& P, int32_t head_dim, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
+void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
                const int32_t (&max_len)[2]) {
     AttnArgs& a = P.a;
     const int hkv = a.C.n_kv_heads;
@@ -1536,12 +1541,15 @@ void plan_attn(AttnPlan& P, int32_t head_dim, const int32_t (&n_prob)[2], const 
     a.join = n_prob[1] > 0 ? 1 : 0;
     a.need_join = a.join;
     const int64_t cols[2] = {(int64_t)max_rows[0] * a.share, (int64_t)max_rows[1] * a.share};   // of a problem, at most
-    // Decode rows behind shared prefixes take one launch for both forms: 32
-    // requests behind 4096 tokens 31 us, in two launches 43.
-    a.together = a.join && cols[0] <= ATTN_FEW_COLS && cols[1] > ATTN_FEW_COLS;
     // 256 columns a tile (8 waves) halve what a column's keys cost to stage;
-    // with fewer columns than that, half of the waves would have none.
-    a.tile_cols = a.together || std::max(cols[0], n_prob[1] > 0 ? cols[1] : 0) <= 128 ? 128 : 256;
+    // with fewer columns than that half of the waves would have none, longer
+    // rows do not leave the registers (kWide), and where the wide tiles would
+    // not fill the card narrow ones go twice as far (twelve prompts behind
+    // three prefixes 103 us, in wide tiles 111).
+    a.decode = cols[0] <= ATTN_FEW_COLS;
+    const int64_t wide_items = ((int64_t)a.B.n_rows * a.share / 256 + std::min(n_prob[0], a.B.n_rows)) * hkv;
+    a.tile_cols = (a.join && a.decode) || head_dim * elem_bytes > 256 || wide_items < 256 ||
+                          std::max(cols[0], n_prob[1] > 0 ? cols[1] : 0) <= 128 ? 128 : 256;
     for (int k = 0; k < 2; ++k) {
         AttnPart& W = a.part[k];
         W = AttnPart{};
@@ -1604,6 +1612,11 @@ void plan_attn(AttnPlan& P, int32_t head_dim, const int32_t (&n_prob)[2], const 
             }
         }
     }
+    // Both forms in one launch where both have work and tiles of 128 columns
+    // do: 32 requests behind a prefix of 4096 tokens 31 us, in two launches
+    // 43; a few fp32 rows and a short prompt 21 us, in two launches 30.
+    a.together = a.tile_cols == 128 && a.part[0].tile_grid + a.part[1].tile_grid > 0 &&
+                 a.part[0].few_grid + a.part[1].few_grid > 0;
     if (a.join) {
         for (int k = 0; k < 2; ++k) {
             P.off[k][6] = take((size_t)a.B.n_rows * a.n_q_heads * ((size_t)head_dim * 4 + sizeof(float2)));

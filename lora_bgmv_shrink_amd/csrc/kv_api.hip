@@ -92,7 +92,7 @@ lora_status_t make_plan(const lora_kv_cache_t* cache, const lora_kv_batch_t* bat
     const int32_t n_prob[2] = {batch->n_seqs, batch->n_groups};
     const int32_t rows[2] = {std::min(batch->max_rows, batch->n_rows), std::min(batch->max_group_rows, batch->n_rows)};
     const int32_t len[2] = {batch->max_kv_len, batch->max_prefix_len};
-    plan_attn(P, cache->head_dim, n_prob, rows, len);
+    plan_attn(P, cache->head_dim, elem_bytes(cache->dtype), n_prob, rows, len);
     return LORA_OK;
 }
 

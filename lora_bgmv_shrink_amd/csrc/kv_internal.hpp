@@ -113,6 +113,7 @@ struct AttnArgs {
     int32_t need_join;
     int32_t tile_cols;          // columns of a tiled item: 128 or 256
     int32_t together;           // both forms in one launch
+    int32_t decode;             // every sequence has few columns
     AttnPart part[2];
 };
 struct AttnPlan {
@@ -121,7 +122,7 @@ struct AttnPlan {
     size_t bytes;
 };
 // max_rows, max_len: host bounds of a problem's rows and keys, per kind
-void plan_attn(AttnPlan& P, int32_t head_dim, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
+void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
                const int32_t (&max_len)[2]);
 hipError_t launch_attn(const AttnArgs& a, lora_dtype_t dt, int32_t head_dim, hipStream_t stream);
 
