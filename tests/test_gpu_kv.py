@@ -98,6 +98,79 @@ def test_long_split():
     attend(Case([40, 1], [5000, 3000], 8, 2, 128, BF, page=64, seed=6), 1500, 9, what="long prompt pieces, window")
 
 
+# Enough rows for the tiles of 256 columns (they have to fill the card).
+WIDE = [
+    # rows, own tokens, prefixes, groups, window, sinks
+    ([700, 1, 0, 430], [720, 300, 10, 450], None, None, 0, 0),
+    ([650, 20, 500], [900, 20, 777], None, None, 200, 5),
+    ([600, 1, 550, 2], [600, 40, 570, 9], [130, 333], [0, 2, 4], 0, 0),
+    ([600, 1, 550, 2], [600, 40, 570, 9], [130, 333], [0, 2, 4], 250, 70),
+    ([1100], [900], [77], [0, 1], 0, 0),     # 200 rows without a place
+]
+
+
+@pytest.mark.parametrize("case", range(len(WIDE)))
+@pytest.mark.parametrize("dtype,d,page", [(BF, 128, 16), (BF, 64, 64), (F32, 64, 2)])
+def test_wide_tiles(case, dtype, d, page):
+    nq, ln, pre, off, window, sinks = WIDE[case]
+    c = Case(nq, ln, 64, 8, d, dtype, page=page, heads_first=case % 2 == 0, prefix=pre, group_off=off, seed=30 + case)
+    attend(c, window, sinks, what="wide")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+def test_wide_tiles_odd_values(bad):
+    """A value that is not finite in a tile of 256 columns reaches the rows from its token on, and only those."""
+    b = binding()
+    c = Case([1100], [1110], 64, 8, 64, BF, seed=36)
+    clean = attend(c, what="wide, clean")
+    t = 640
+    c.cpu_v[c.pages[0][t // 16], t % 16, :, 5] = bad
+    say(f"wide, odd value {bad}")
+    got = b.lora_attn_paged(c.cache(b), c.batch(b), c.q.to(DEV), 0.125)
+    torch.cuda.synchronize()
+    got = got.double().cpu()
+    sees = t - 10     # row r is at position r + 10
+    assert torch.equal(got[:sees], clean[:sees])
+    after = got[sees:].view(-1, 64, 64)
+    assert not torch.isfinite(after[:, :, 5]).any()
+    assert torch.isfinite(after[:, :, :5]).all() and torch.isfinite(after[:, :, 6:]).all()
+
+
+def test_scores_that_jump():
+    """Scores that grow by hundreds from one tile to the next: the softmax's reference has to follow them."""
+    for nq, ln, hq, hkv in (([1, 1], [900, 33], 8, 2), ([300], [700], 8, 2), ([1100], [1100], 64, 8)):
+        c = Case(nq, ln, hq, hkv, 64, F32, page=64, seed=37)
+        for s, pages in enumerate(c.pages):
+            k, v = c.own[s]
+            up = (1.0 + 4.0 * (torch.arange(ln[s]) // 150)).view(-1, 1, 1)
+            k *= up
+            for t in range(0, ln[s], c.page):
+                m = min(c.page, ln[s] - t)
+                c.cpu_k[pages[t // c.page], :m] = k[t:t + m].float()
+        b = binding()
+        say(f"jumping scores: rows {nq} tokens {ln}")
+        lse = torch.empty((c.n_rows, hq), device=DEV)
+        o = b.lora_attn_paged(c.cache(b), c.batch(b), c.q.to(DEV), 1.0, lse=lse)
+        torch.cuda.synchronize()
+        ro, rl = c.reference(1.0)
+        # scores of up to about 1000: fp32 sums err by 2^-24 * 64 * 1000 at the very most, 4e-3, and o by twice that
+        assert float((lse.double().cpu() - rl).abs().max()) <= 4e-3
+        assert float((o.double().cpu() - ro).abs().max()) <= 8e-3 * vmax(c)
+
+
+@pytest.mark.parametrize("heads", [(20, 1), (34, 2), (64, 2)], ids=lambda h: f"{h[0]}on{h[1]}")
+def test_prefix_many_heads_per_key_head(heads):
+    """More than 16 query heads on one key head: even one row takes the tiled form, and walks its prefix itself."""
+    attend(Case([1, 1, 9, 1], [5, 300, 9, 40], *heads, 64, BF, prefix=[500, 70], group_off=[0, 2, 4], seed=38), what="heads")
+
+
+def test_prefix_split():
+    """A long prefix whose tiles are split among workgroups, for decode rows and beside prompts."""
+    attend(Case([1] * 20, [30] * 20, 8, 2, 128, BF, prefix=[9000], group_off=[0, 20], page=64, seed=39), what="split prefix")
+    attend(Case([1] * 20 + [40], [30] * 20 + [50], 8, 2, 128, BF, prefix=[9000], group_off=[0, 21], page=64, seed=40),
+           what="split prefix beside a prompt")
+
+
 @pytest.mark.parametrize("page", [1, 2, 4, 128, 1024])
 def test_page_sizes(page):
     attend(Case([1, 30, 1], [77, 190, 400], 8, 2, 64, BF, page=page, seed=7), what="page")
