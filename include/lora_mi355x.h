@@ -737,9 +737,10 @@ lora_status_t lora_kv_append(const lora_kv_cache_t* cache, const lora_kv_batch_t
  *   status (device, may be NULL) gets bit 0 set when a page number that some
  *   row needs is outside [0, n_pages); its tokens are then not seen.
  * Results do not depend on timing.  lora_attn_paged takes a batch without
- * groups.  lora_attn_prefix takes one with groups: the prefix's keys and
- * values are read once per group for all its rows, and each row's partial
- * results over the prefix and over its own tokens are joined in fp32.
+ * groups.  lora_attn_prefix takes one with groups: sequences of up to 16
+ * columns (rows times G; a decode step's) share one reading of their group's
+ * prefix, and the partial results over the prefix and over a row's own tokens
+ * are joined in fp32; a longer sequence's rows walk both in one go.
  * The workspace (lora_attn_workspace, for either entry point and any window)
  * holds partial results only; it needs no zero-filling, and any content is
  * left in it. */

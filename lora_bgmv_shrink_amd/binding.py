@@ -679,7 +679,7 @@ def lora_attn_prefix(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: flo
                      lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                      ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """lora_attn_paged for a batch whose groups of sequences share a prefix,
-    whose keys and values are read once per group."""
+    which a group's decode rows read once together."""
     return _attn(_lib.lora_attn_prefix, "lora_attn_prefix", cache, batch, q, scale, window, n_sink, o, o_dtype, lse,
                  status, ws)
 

@@ -5,7 +5,7 @@
 // a row at position p seeing key k when k <= p and, with a window, when
 // k > p - window or k < n_sink.
 //
-// Both kernels form the transposed products: S^T = K Q^T, then O^T = V^T P^T.
+// Both forms (few query columns, many) make the transposed products: S^T = K Q^T, then O^T = V^T P^T.
 // The matrix cores' output layout puts one query column in each lane, so the
 // running maximum and sum of the softmax are one register a lane, a column's
 // scores are folded by one or two lane exchanges, and the rounded weights are
@@ -14,7 +14,8 @@
 // a product's sum may run in any order, so V is read in that same order, by
 // LDS transpose reads.)  Scores, the statistics and O are fp32; the weights
 // P are rounded to the cache's type for the second product, each by at most
-// 2^-9 of itself in bf16, the rounding o itself gets at the end.
+// 2^-8 of itself in bf16, the rounding o itself gets at the end; they are
+// summed for the softmax before they are rounded.
 #include "kv_internal.hpp"
 
 namespace lora {
@@ -609,10 +610,16 @@ __device__ __forceinline__ uint64_t sees(const AttnArgs& a, int col_pos, int lo,
 // takes 32 of them through LDS of its own (no barrier; values take the keys'
 // place once those are multiplied, so that three workgroups fit a CU), with
 // the next unit's pieces in flight in registers and the unit after's page
-// numbers before them.  Shared form (few = 2): the units of all problems are dealt to the
-// workgroups in equal runs, whatever the lengths; a run's first and last
-// (problem, head) may be partial and go to slots that the join adds.
+// numbers before them.  Shared form (few = 2): the units of all problems are
+// dealt to the workgroups in equal runs, whatever the lengths; a run's first
+// and last (problem, head) may be partial and go to slots that the join adds.
 // Otherwise a workgroup takes one (problem, head) whole.
+//
+// bf16, 8 key heads of 128, 8 sequences of 16 k to 60 k tokens: 189 us, 1.14
+// GB, 6.0 TB/s (a plain read of this shape: 6.5); 256 sequences that see 1024
+// tokens and 4 sinks: 180 us, 5.6 TB/s; 32 sequences of up to 2048 tokens: 31
+// us, 4.3 TB/s, of which some 6 us are a piece's beginning (its problem, its
+// q, its first keys: loads that depend on one another) and its end.
 template <typename T, int D>
 struct FewStage {   // LDS of a wave: 32 keys, or 16 columns of O and their statistics
     static constexpr int KEYS = ATTN_FEW_KEYS / 4 * Tile<T, D>::RB, OUT = 16 * (D + 4) * 4 + 128;
@@ -935,14 +942,24 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
 // Many query columns (prompts, shared prefixes): the columns are split
 // ---------------------------------------------------------------------------
 
-// A workgroup owns 128 columns of one key head, 32 a wave, and walks tiles of
-// 64 keys staged in LDS, two buffers, the next tile's pieces in flight in
-// registers meanwhile: one barrier a tile.  Each staged byte feeds 128
-// columns, 4 D flop per key and column, so the matrix cores bound it.  Items
-// (problem, column tile, key head, run of key tiles) are numbered with the
-// key head fastest, so that the columns of one head meet in one XCD's L2, and
-// later column tiles (more keys under the causal mask) first.
-// Rows of up to 256 bytes leave the registers for tiles of 256 columns.
+// A workgroup owns 128 or 256 columns of one key head, 32 a wave, and walks
+// tiles of 64 keys that its waves load straight into LDS: two buffers, one
+// barrier a tile, the next tile's loads spread over this one's products.  Each
+// staged byte feeds all columns, 4 D flop per key and column, so the matrix
+// cores bound it; a wave's two halves of 32 keys let them work on one half
+// while the vector units make weights of the other.  Items (problem, column
+// tile, key head, run of key tiles) are numbered with the key head fastest,
+// so that the columns of one head meet in one XCD's L2, and later column
+// tiles (more keys under the causal mask) first.
+//
+// bf16, 32 heads on 8 of 128, a prompt of 8192 tokens: 582 us, 945 TFLOP/s of
+// the 1232 that a large matrix product reaches; 64 heads on 8, 2048 rows that
+// see 4096 tokens of 10 k: 169 us, 510 TFLOP/s (256 items of unequal length
+// on 256 CUs).  A tile of 64 keys by 256 columns takes 2.5 us, of them 1.1 at
+// the matrix cores' rate; the rest is LDS reads' latency, the waves' skew at
+// the barrier and the softmax's vector work.
+//
+// Only rows of up to 256 bytes leave the registers for tiles of 256 columns.
 template <typename T, int D> constexpr bool kWide = sizeof(T) * D <= 256;
 template <typename T, int D, bool PAGED, int NW>
 __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block, uint8_t* stage, int* sh) {
@@ -1226,27 +1243,27 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
                              __attribute__((always_inline)) { acc[t] = O::mma32(vf, x, acc[t]); });
                 sched_mix<T, 4, D / 8, 2, 0, 0>();
             } else {
-            products([&](typename O::frag vf, const typename O::frag& x, int t) __attribute__((always_inline)) {
-                O::clean(vf);
-                acc[t] = O::mma32(vf, x, acc[t]);
-            });
-            const uint64_t seen = sees(a, col_pos, lo, bits_i);
-            for (int k = 0; k < KB; ++k) {
-                const int e = ((k >> 3) & 3) * 4 + (k & 3);
-                float x = 0.f;
+                products([&](typename O::frag vf, const typename O::frag& x, int t) __attribute__((always_inline)) {
+                    O::clean(vf);
+                    acc[t] = O::mma32(vf, x, acc[t]);
+                });
+                const uint64_t seen = sees(a, col_pos, lo, bits_i);
+                for (int k = 0; k < KB; ++k) {
+                    const int e = ((k >> 3) & 3) * 4 + (k & 3);
+                    float x = 0.f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (r == e) x = k < 32 ? w[0][r] : w[1][r];
-                x = __shfl(x, ((k >> 2) & 1) * 32 + l32, 64);
-                if (!((seen >> k) & 1)) continue;
+                    for (int r = 0; r < 16; ++r)
+                        if (r == e) x = k < 32 ? w[0][r] : w[1][r];
+                    x = __shfl(x, ((k >> 2) & 1) * 32 + l32, 64);
+                    if (!((seen >> k) & 1)) continue;
 #pragma unroll
-                for (int t = 0; t < D / 32; ++t)
+                    for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float y = TL::v_one(sv, k, t * 32 + 8 * (r >> 2) + 4 * h2 + (r & 3));
-                        if (non_finite(y)) acc[t][r] += x * y;
-                    }
-            }
+                        for (int r = 0; r < 16; ++r) {
+                            const float y = TL::v_one(sv, k, t * 32 + 8 * (r >> 2) + 4 * h2 + (r & 3));
+                            if (non_finite(y)) acc[t][r] += x * y;
+                        }
+                }
             }
         }
         for (int i = iw; i < i1; ++i) arrive(i, 4);
@@ -1301,7 +1318,9 @@ void k_attn_tile(AttnArgs a) {
 // Both forms in one launch, side by side (decode rows behind a shared prefix:
 // the tiled form over the prefix, the few-column form over the rows' own
 // tokens): their workgroups alternate, eight by eight so that each kind still
-// goes round the XCDs.
+// goes round the XCDs, and the one's matrix products run beside the other's
+// reads.  256 requests behind eight prefixes of 1000 to 8000 tokens, 64 heads
+// on 8: 226 us with the join, 0.72 GB and 4.9e10 flop.
 template <typename T, int D, bool PAGED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) * D <= 256 ? 2 : 1)))
 void k_attn_both(AttnArgs a) {
@@ -1341,8 +1360,9 @@ void k_attn_both(AttnArgs a) {
 // four); every partial result is read once.
 //
 // by_row: all rows (split tiled items).  Otherwise only rows of few-column
-// sequences can have partial results, and the waves are
-// numbered by (sequence, row in it) so that a prompt's rows cost nothing.
+// sequences can have partial results, and the waves are numbered by
+// (sequence, row in it) so that a prompt's rows cost nothing.
+// 32 rows of 32 heads: 9 us with its launch, nearly all of it latency.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int by_row, int rows_of_few) {
     constexpr int N = D / 16;   // elements per lane

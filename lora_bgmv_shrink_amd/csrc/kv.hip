@@ -7,8 +7,10 @@
 // Every element is read once and written once, in fp32 between, rounded once
 // into the cache's type: 2 * rows * (heads of q, k and v) * head_dim elements
 // plus 4 bytes per pair and row of the tables, 6 flop per pair.  Bytes bound
-// for prompts; for one decode step the time is the chain of dependent loads
-// (row's sequence -> its length -> its page -> the store).
+// for prompts (20304 rows of 64 heads on 8 of 128, bf16: 163 us, 5.1 TB/s, the
+// rate of a plain copy); for one decode step the time is the chain of
+// dependent loads (row's sequence -> its length -> its page -> the store): 32
+// rows of 32 heads on 8, 3.9 us.
 #include "kv_internal.hpp"
 
 namespace lora {
