@@ -528,20 +528,25 @@ __device__ __forceinline__ void sched_mix() {
 
 // Direct loads from memory to LDS: lane i's 16 bytes go to `to` + 16 i.  The
 // staged tile lies in rows of the pieces' permuted order, so a lane asks for
-// the piece that belongs at its place.  landed() waits for them; the compiler
+// the piece that belongs at its place.  M0 names the place; it is the
+// compiler's register, and put back at once.  landed() waits for them; the compiler
 // does not count them, and its own waits, which count fewer loads than are
 // out, come out later and never earlier than they must.
 __device__ __forceinline__ void lds_load(const void* base, uint32_t off, uint32_t to) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)base);
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uintptr_t)base >> 32));
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off),
-                 "s"(((uint64_t)hi << 32) | lo), "s"(__builtin_amdgcn_readfirstlane(to))
-                 : "memory", "m0");
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "v"(off), "s"(((uint64_t)hi << 32) | lo), "s"(__builtin_amdgcn_readfirstlane(to))
+                 : "memory");
 }
 __device__ __forceinline__ void lds_load(const void* at, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(at),
-                 "s"(__builtin_amdgcn_readfirstlane(to))
-                 : "memory", "m0");
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "v"(at), "s"(__builtin_amdgcn_readfirstlane(to))
+                 : "memory");
 }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
