@@ -957,7 +957,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
 // so that the columns of one head meet in one XCD's L2, and later column
 // tiles (more keys under the causal mask) first.
 //
-// bf16, 32 heads on 8 of 128, a prompt of 8192 tokens: 582 us, 945 TFLOP/s of
+// bf16, 32 heads on 8 of 128, a prompt of 8192 tokens: 580 us, 948 TFLOP/s of
 // the 1232 that a large matrix product reaches; 64 heads on 8, 2048 rows that
 // see 4096 tokens of 10 k: 169 us, 510 TFLOP/s (256 items of unequal length
 // on 256 CUs).  A tile of 64 keys by 256 columns takes 2.5 us, of them 1.1 at
