@@ -815,7 +815,9 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
         // rows do not see (0 times them is NaN) are looked for in the units
         // that rows see in part; where there are some (the answer) the walk is
         // made again with ODD, which leaves them out of the product and adds
-        // them to the columns that see them.
+        // them to the columns that see them.  One row of a sequence sees just
+        // what `bits` says; one row of a group may sit any number of tokens
+        // behind the prefix, past keys that the least position still sees.
         auto walk = [&](auto ODD) __attribute__((always_inline)) {
             m = -kInf;
             l = 0.f;
@@ -843,7 +845,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
                     if (!all_see) {
                         asm volatile("");
                         hide_rows<NL>(rv, bits_x, here(lane) / TL::LPR, RPL);
-                        if (!ODD && P.nr > 1) {
+                        if (!ODD && (P.nr > 1 || kind == 1)) {
 #pragma unroll
                             for (int j = 0; j < NL; ++j) odd |= odd_piece<T>(rv[j]);
                         }

@@ -502,3 +502,41 @@ def test_empty_batch():
     o = b.lora_attn_paged(cache, batch, q, 0.125)
     torch.cuda.synchronize()
     assert o.shape == (0, 256)
+
+
+# rows and own tokens of the sequences of one group: one row alone (a sequence whose row sits some tokens behind the
+# prefix), a few rows, enough for the tiled form, and a prompt beside a decode row
+ODD_PREFIX = [([1], [9]), ([1], [3]), ([1, 1], [40, 3]), ([1] * 30, [3, 9] * 15), ([1, 25], [9, 60])]
+
+
+@pytest.mark.parametrize("case", range(len(ODD_PREFIX)))
+@pytest.mark.parametrize("dtype,d,heads", [(BF, 128, (2, 2)), (BF, 64, (8, 2)), (BF, 64, (32, 2)), (F32, 64, (4, 2))])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 2)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_odd_values_in_a_prefix(case, dtype, d, heads, window, sinks, bad):
+    """A key or value of a shared prefix that is not finite reaches the rows whose window holds it, and only those."""
+    b = binding()
+    nq, ln = ODD_PREFIX[case]
+    hq, hkv = heads
+    n, t = 200, 155
+    c = Case(nq, ln, hq, hkv, d, dtype, prefix=[n], group_off=[0, len(nq)], seed=41)
+    clean = attend(c, window, sinks, what="clean prefix")
+    pg, at = c.prefix_pages[0][t // c.page], t % c.page
+    c.cpu_v[pg, at, :, 3] = bad
+    c.cpu_k[pg, at, 1, 0] = bad
+    say(f"odd values in a prefix: {bad}")
+    got = b.lora_attn_prefix(c.cache(b), c.batch(b), c.q.to(DEV), 1.0 / math.sqrt(d), window=window, n_sink=sinks)
+    torch.cuda.synchronize()
+    got = got.double().cpu()
+    row = 0
+    for s, rows in enumerate(nq):
+        for j in range(rows):
+            p = n + ln[s] - rows + j
+            x = got[row].view(hkv, -1, d)
+            if window and t <= p - window:
+                assert torch.equal(got[row], clean[row]), (s, j)
+            else:
+                # the heads of key head 0 have finite scores and the odd value in dimension 3
+                assert not torch.isfinite(x[0, :, 3]).any(), (s, j)
+                assert torch.isfinite(x[0, :, :3]).all() and torch.isfinite(x[0, :, 4:]).all(), (s, j)
+            row += 1
