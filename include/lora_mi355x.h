@@ -743,7 +743,9 @@ lora_status_t lora_kv_append(const lora_kv_cache_t* cache, const lora_kv_batch_t
  * are joined in fp32; a longer sequence's rows walk both in one go.
  * The workspace (lora_attn_workspace, for either entry point and any window)
  * holds partial results only; it needs no zero-filling, and any content is
- * left in it. */
+ * left in it.  Its size grows with n_seqs, n_rows, n_groups and the max_
+ * bounds: one queried for a server's largest batch serves, with the same
+ * cache and n_q_heads, every batch none of whose bounds is larger. */
 lora_status_t lora_attn_workspace(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, int32_t n_q_heads,
                                   size_t* bytes);
 lora_status_t lora_attn_paged(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, const void* q, int64_t ldq,

@@ -638,7 +638,8 @@ def lora_attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> int:
 
 def attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> torch.Tensor:
     """A workspace for either attention over this batch (or one with no
-    larger bounds), for calls that do not overlap in time."""
+    larger bounds: sequences, rows, groups and the host bounds), for calls
+    that do not overlap in time."""
     return torch.empty(lora_attn_workspace(cache, batch, n_q_heads), dtype=torch.uint8, device=cache.device)
 
 

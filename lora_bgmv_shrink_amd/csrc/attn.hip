@@ -1557,6 +1557,9 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 
 void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
                const int32_t (&max_len)[2]) {
+    // The workspace's parts grow with every bound and do not rest on the
+    // window (with one there are fewer keys, so fewer shared units and no more
+    // splits), so that one allocation serves every smaller batch.
     AttnArgs& a = P.a;
     const int hkv = a.C.n_kv_heads;
     size_t at = 0;
@@ -1584,9 +1587,7 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
         W.max_len = max_len[k];
         for (size_t& o : P.off[k]) o = 0;
         if (n_prob[k] <= 0) continue;
-        // the keys that a problem's tiles span.  The workspace does not rest on
-        // the window: with one there are fewer keys, so fewer shared units, and
-        // no more splits than the bound `most` below.
+        // the keys that a problem's tiles span
         int64_t reach = max_len[k];
         if (a.window > 0) reach = std::min<int64_t>(reach, (int64_t)a.window + max_rows[k] + a.n_sink + 256);
         if (a.share <= ATTN_FEW_COLS) {
@@ -1599,11 +1600,13 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
             // with a window of 1024 180 us, in shares 220.  And where there
             // is little to share (4 units).  Otherwise equal shares: 8
             // requests of 16k to 60k tokens on 8 heads would be 64 pairs.
-            auto direct = [&](int64_t u) { return u <= 4 || (heads >= 256 && u <= 16) || heads >= 4096; };
-            W.few = direct(units) ? 1 : 2;
+            auto direct = [](int64_t u, int64_t pairs) {
+                return u <= 4 || (pairs >= 256 && u <= 16) || pairs >= 4096;
+            };
+            W.few = direct(units, heads) ? 1 : 2;
             W.few_grid = W.few == 1 ? n_prob[k] * hkv : ATTN_FEW_WGS;
             if (W.few == 2) a.need_join = 1;
-            if (!direct(ceil_div(max_len[k], ATTN_FEW_KEYS))) {
+            if (!direct(ceil_div(max_len[k], ATTN_FEW_KEYS), hkv)) {   // of a single sequence or group
                 P.off[k][0] = take((size_t)n_prob[k] * hkv * sizeof(int2));
                 P.off[k][1] = take((size_t)2 * ATTN_FEW_WGS * 16 * head_dim * 4);
                 P.off[k][2] = take((size_t)2 * ATTN_FEW_WGS * 16 * sizeof(float2));
@@ -1632,10 +1635,20 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
             W.tile_grid = (int32_t)(items * ns);
             W.slots = ns > 1 ? 1 : 0;
             if (W.slots) a.need_join = 1;
-            if (most > 1) {
+            // Room for the partial results of any smaller batch too: it splits
+            // min(want / items, most_tiles / 4) ways into at most `want` items
+            // and at most most_tiles / 4 times its own, in narrow tiles where
+            // this one's are.  Sequences in wide tiles are `want` items or
+            // more and never split.
+            if (most_tiles >= 8) {
+                auto columns = [&](int tc) {
+                    const int64_t most_items = ((int64_t)a.B.n_rows * a.share / tc + std::min(n_prob[k], a.B.n_rows)) * hkv;
+                    return std::min(want, most_items * (most_tiles / 4)) * tc;
+                };
+                const size_t cols = (size_t)std::max(columns(128), k == 1 && a.tile_cols == 256 ? columns(256) : 0);
                 P.off[k][3] = take((size_t)n_prob[k] * sizeof(int4));
-                P.off[k][4] = take((size_t)(nct * hkv * most) * a.tile_cols * head_dim * 4);
-                P.off[k][5] = take((size_t)(nct * hkv * most) * a.tile_cols * sizeof(float2));
+                P.off[k][4] = take(cols * head_dim * 4);
+                P.off[k][5] = take(cols * sizeof(float2));
             }
         }
     }

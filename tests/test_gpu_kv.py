@@ -540,3 +540,20 @@ def test_odd_values_in_a_prefix(case, dtype, d, heads, window, sinks, bad):
                 assert not torch.isfinite(x[0, :, 3]).any(), (s, j)
                 assert torch.isfinite(x[0, :, :3]).all() and torch.isfinite(x[0, :, 4:]).all(), (s, j)
             row += 1
+
+
+def test_one_workspace_for_a_shrinking_batch():
+    """The workspace of a server's largest batch serves its smaller ones; nothing is written past its size."""
+    b = binding()
+    hq, hkv, d = 32, 8, 64
+
+    def case(n, seed):
+        return Case([1] * n + [30], [2000 - 40 * i for i in range(n)] + [700], hq, hkv, d, BF, page=64, seed=seed)
+
+    c = case(33, 42)
+    need = b.lora_attn_workspace(c.cache(b), c.batch(b), hq)
+    whole = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    for n in (33, 31, 5, 1):
+        for window in (0, 900):
+            attend(case(n, 42 + n), window, 3 if window else 0, what=f"{n} decode rows and a prompt", ws=whole[:need])
+            assert bool((whole[need:] == 0xA5).all())

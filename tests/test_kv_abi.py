@@ -121,3 +121,58 @@ def test_no_rows_is_a_no_op():
     assert attn(b, cache, batch) in (b.LORA_OK, b.LORA_E_WORKSPACE)
     batch.n_seqs = 0
     assert attn(b, cache, batch, ws=None) == b.LORA_OK
+
+
+def workspace(b, cache, batch, hq):
+    n = ctypes.c_size_t()
+    assert b.library().lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), hq, ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_workspace_serves_smaller_bounds(seed):
+    """A workspace for a batch's bounds holds every batch whose bounds are no larger, one without groups too."""
+    import random
+    rng = random.Random(seed)
+    b, cache, _, _ = structs()
+    hq, cache.n_kv_heads = rng.choice([(32, 8), (64, 8), (4, 4), (20, 1), (64, 2), (5, 1), (512, 256)])
+    cache.dtype, cache.head_dim = rng.choice([(b.LORA_BF16, 64), (b.LORA_BF16, 128), (b.LORA_BF16, 256), (b.LORA_F32, 128)])
+    cache.page_stride, cache.token_stride, cache.head_stride = 1 << 20, cache.head_dim, 16 * cache.head_dim
+
+    def size(n_seqs, n_rows, max_rows, max_kv_len, n_groups, max_prefix, max_group_rows):
+        batch = b.KvBatchT(FAKE, FAKE, FAKE, 4, n_seqs, n_rows, max_rows, max_kv_len, FAKE, FAKE, FAKE, 4, n_groups,
+                           max_prefix, max_group_rows)
+        return workspace(b, cache, batch, hq)
+
+    def upto(n):
+        return rng.choice([n, n, max(1, n - 1), max(1, n // 2), max(1, n // 3), rng.randint(1, n)])
+
+    for _ in range(200):
+        most = [rng.choice([1, 8, 32, 33, 200, 600, 5000]), rng.choice([1, 32, 100, 900, 4096, 20000]),
+                rng.choice([1, 4, 5, 17, 100, 4096]), rng.choice([1, 128, 512, 513, 2047, 2048, 2049, 9000, 60000]),
+                rng.choice([0, 1, 3, 8, 600]), rng.choice([1, 64, 2500, 9000]), rng.choice([1, 4, 32, 300, 4096])]
+        large = size(*most)
+        for _ in range(20):
+            less = [upto(n) if n else 0 for n in most]
+            if rng.random() < 0.2:
+                less[4] = 0
+            small = size(*less)
+            assert small <= large, (most, large, less, small)
+
+
+def test_workspace_serves_a_shrinking_server():
+    """32 requests of up to 2048 tokens, and what is left of them; a long prompt, and a short one."""
+    b, cache, batch, _ = structs()
+    cache.n_kv_heads, cache.head_dim, cache.token_stride, cache.head_stride = 8, 128, 128, 16 * 128
+    cache.page_stride = 8 * 16 * 128
+    batch.max_rows, batch.max_kv_len = 1, 2048
+    sizes = []
+    for n in (32, 31, 8, 1):
+        batch.n_seqs = batch.n_rows = n
+        sizes.append(workspace(b, cache, batch, 32))
+    assert sizes == sorted(sizes, reverse=True), sizes
+    batch.n_seqs, batch.max_kv_len, sizes = 1, 8192, []
+    for n in (4096, 256, 100, 5):
+        batch.n_rows = batch.max_rows = n
+        sizes.append(workspace(b, cache, batch, 32))
+    assert sizes == sorted(sizes, reverse=True), sizes
