@@ -556,12 +556,14 @@ class KvCache:
 
 class KvBatch:
     """One step's sequences (lora_kv_batch_t): int32 device tensors, and the
-    host bounds that size launches and workspaces.  The tensors are kept, so
-    their contents may be changed in place within the bounds."""
+    host bounds that size launches and workspaces (of the prefixes too, where
+    there are groups).  The tensors are kept, so their contents may be changed
+    in place within the bounds."""
 
     def __init__(self, row_off: torch.Tensor, kv_len: torch.Tensor, pages: torch.Tensor, n_rows: int, max_rows: int,
                  max_kv_len: int, group_off: Optional[torch.Tensor] = None, prefix_len: Optional[torch.Tensor] = None,
-                 prefix_pages: Optional[torch.Tensor] = None, max_prefix_len: int = 0, max_group_rows: int = 0):
+                 prefix_pages: Optional[torch.Tensor] = None, max_prefix_len: Optional[int] = None,
+                 max_group_rows: Optional[int] = None):
         for t in (row_off, kv_len, pages, group_off, prefix_len, prefix_pages):
             assert t is None or (t.is_cuda and t.dtype == torch.int32), "int32 device tensors"
         for t in (row_off, kv_len, group_off, prefix_len):
@@ -570,13 +572,17 @@ class KvBatch:
         assert row_off.numel() == n_seqs + 1 and pages.shape[0] == n_seqs
         n_groups = 0 if group_off is None else group_off.numel() - 1
         if n_groups:
+            assert prefix_len is not None and prefix_pages is not None, "groups have prefix_len and prefix_pages"
             assert prefix_len.numel() == n_groups and prefix_pages.shape[0] == n_groups
+            # what lies past a bound is not computed, so none is assumed
+            assert max_prefix_len is not None and max_group_rows is not None, \
+                "groups have the bounds max_prefix_len and max_group_rows"
         self.tensors = (row_off, kv_len, pages, group_off, prefix_len, prefix_pages)
         self.n_seqs, self.n_rows, self.n_groups = n_seqs, int(n_rows), n_groups
         ptr = [None if t is None else t.data_ptr() for t in self.tensors]
         self.struct = KvBatchT(ptr[0], ptr[1], ptr[2], self._width(pages), n_seqs, self.n_rows, int(max_rows),
                                int(max_kv_len), ptr[3], ptr[4], ptr[5], self._width(prefix_pages) if n_groups else 0,
-                               n_groups, int(max_prefix_len), int(max_group_rows))
+                               n_groups, int(max_prefix_len or 0), int(max_group_rows or 0))
         self.ref = ctypes.addressof(self.struct)
 
     @staticmethod
