@@ -547,7 +547,7 @@ class KvCache:
         assert k.is_cuda and v.is_cuda and k.dim() == 4 and k.dtype == v.dtype and k.device == v.device
         assert k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1, \
             "k and v: one shape, equal strides, head_dim contiguous"
-        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = (int(n) for n in k.shape)
         self.struct = KvCacheT(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), _dt(k.dtype),
                                self.n_pages, self.page_size, self.n_kv_heads, self.head_dim)
@@ -564,8 +564,10 @@ class KvBatch:
                  max_kv_len: int, group_off: Optional[torch.Tensor] = None, prefix_len: Optional[torch.Tensor] = None,
                  prefix_pages: Optional[torch.Tensor] = None, max_prefix_len: Optional[int] = None,
                  max_group_rows: Optional[int] = None):
+        self.index = row_off.get_device()
         for t in (row_off, kv_len, pages, group_off, prefix_len, prefix_pages):
-            assert t is None or (t.is_cuda and t.dtype == torch.int32), "int32 device tensors"
+            assert t is None or (t.is_cuda and t.get_device() == self.index and t.dtype == torch.int32), \
+                "int32 tensors of one device"
         for t in (row_off, kv_len, group_off, prefix_len):
             assert t is None or (t.dim() == 1 and t.is_contiguous())
         n_seqs = kv_len.numel()
@@ -596,18 +598,25 @@ class Rope:
     """Rotary tables: ``cos`` and ``sin`` fp32 [n_pos, rot_dim / 2]."""
 
     def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
-        assert cos.is_cuda and cos.dtype == sin.dtype == torch.float32 and cos.shape == sin.shape
+        assert cos.is_cuda and sin.is_cuda and cos.get_device() == sin.get_device() and cos.dtype == sin.dtype == torch.float32 and cos.shape == sin.shape
         assert cos.dim() == 2 and cos.stride() == sin.stride() and cos.stride(1) == 1
-        self.cos, self.sin = cos, sin
+        self.cos, self.sin, self.index = cos, sin, cos.get_device()
         self.struct = RopeT(cos.data_ptr(), sin.data_ptr(), cos.stride(0), cos.shape[0], 2 * cos.shape[1],
                             int(bool(interleaved)))
         self.ref = ctypes.addressof(self.struct)
 
 
-def _heads(t: torch.Tensor, rows: int, d: int) -> int:
-    assert t.is_cuda and t.dim() == 2 and t.stride(1) == 1 and t.shape[0] == rows and t.shape[1] % d == 0, \
+def _heads(t: torch.Tensor, cache: KvCache, rows: int) -> int:
+    d = cache.head_dim
+    assert t.is_cuda and t.get_device() == cache.index, "a tensor of the cache's device"
+    assert t.dim() == 2 and t.stride(1) == 1 and t.shape[0] == rows and t.shape[1] % d == 0, \
         "expected [n_rows, heads * head_dim], row-major"
     return t.shape[1] // d
+
+
+def _here(t: Optional[torch.Tensor], cache: KvCache, dtype: torch.dtype) -> bool:
+    """An optional tensor of the cache's device (or none)."""
+    return t is None or (t.is_cuda and t.get_device() == cache.index and t.dtype == dtype and t.numel() > 0)
 
 
 def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
@@ -617,15 +626,16 @@ def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k:
     the rotated q in the cache's type (``q_out``, allocated when not given;
     None without q)."""
     n, d = batch.n_rows, cache.head_dim
-    assert k.dtype == v.dtype and _heads(k, n, d) == cache.n_kv_heads == _heads(v, n, d)
+    assert batch.index == cache.index and (rope is None or rope.index == cache.index), "tensors of the cache's device"
+    assert k.dtype == v.dtype and _heads(k, cache, n) == cache.n_kv_heads == _heads(v, cache, n)
     hq = 0
     if q is not None:
-        hq = _heads(q, n, d)
+        hq = _heads(q, cache, n)
         assert q.dtype == k.dtype
         if q_out is None:
             q_out = torch.empty((n, hq * d), dtype=cache.dtype, device=q.device)
-        assert q_out.dtype == cache.dtype and _heads(q_out, n, d) == hq
-    assert status is None or status.dtype == torch.int32
+        assert q_out.dtype == cache.dtype and _heads(q_out, cache, n) == hq
+    assert _here(status, cache, torch.int32), "status: int32, of the cache's device"
     st = _lib.lora_kv_append(cache.ref, batch.ref, None if rope is None else rope.ref, _dt(k.dtype),
                              q.data_ptr() if hq else None, q.stride(0) if hq else 0, hq, k.data_ptr(), k.stride(0),
                              v.data_ptr(), v.stride(0), q_out.data_ptr() if hq else None,
@@ -653,19 +663,22 @@ def _attn(fn, where: str, cache: KvCache, batch: KvBatch, q: torch.Tensor, scale
           o: Optional[torch.Tensor], o_dtype: Optional[torch.dtype], lse: Optional[torch.Tensor],
           status: Optional[torch.Tensor], ws: Optional[torch.Tensor]) -> torch.Tensor:
     n, d = batch.n_rows, cache.head_dim
-    hq = _heads(q, n, d)
+    assert batch.index == cache.index, "tensors of the cache's device"
+    hq = _heads(q, cache, n)
     assert q.dtype == cache.dtype, "q has the cache's type"
     if o is None:
         o = torch.empty((n, hq * d), dtype=o_dtype or cache.dtype, device=q.device)
-    assert _heads(o, n, d) == hq
+    assert _heads(o, cache, n) == hq
     if lse is not None:
-        assert lse.dtype == torch.float32 and lse.shape == (n, hq) and lse.is_contiguous()
-    assert status is None or status.dtype == torch.int32
+        assert lse.is_cuda and lse.get_device() == cache.index and lse.dtype == torch.float32
+        assert lse.shape == (n, hq) and lse.is_contiguous()
+    assert _here(status, cache, torch.int32), "status: int32, of the cache's device"
     if ws is None:
         ws = attn_workspace(cache, batch, hq)
+    assert ws.is_cuda and ws.get_device() == cache.index and ws.is_contiguous(), "a workspace of the cache's device"
     st = fn(cache.ref, batch.ref, q.data_ptr(), q.stride(0), hq, scale, window, n_sink, o.data_ptr(), _dt(o.dtype),
             o.stride(0), None if lse is None else lse.data_ptr(), None if status is None else status.data_ptr(),
-            ws.data_ptr(), ws.numel(), _stream(q.device))
+            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(q.device))
     if st:
         _check(st, where)
     return o
