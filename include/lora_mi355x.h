@@ -667,7 +667,8 @@ typedef struct {
  *   kv_len[n_seqs]       its tokens in its own pages, this step's rows
  *                        included (they are the last ones);
  *   pages[n_seqs, ldp]   its page numbers: token t is in page
- *                        pages[s, t / page_size];
+ *                        pages[s, t / page_size]; NULL only with ldp = 0
+ *                        (prefix_pages alike);
  *   max_rows, max_kv_len host bounds of a sequence's rows and tokens.  They
  *                        size the launches and the workspace; rows and tokens
  *                        past them are not computed or not seen.

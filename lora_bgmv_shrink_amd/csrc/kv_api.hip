@@ -51,10 +51,12 @@ lora_status_t check_batch(const lora_kv_batch_t* b, KvBatchDev& B) {
     if (b->max_rows < 0 || b->max_kv_len < 0 || b->ldp < 0 || b->max_group_rows < 0 || b->max_prefix_len < 0 ||
         b->ldpp < 0)
         return LORA_E_INVALID;
-    if (b->n_seqs > 0 && (!b->row_off || !b->kv_len || !b->pages || !al4(b->row_off) || !al4(b->kv_len) || !al4(b->pages)))
+    // a table of no columns is never read, and may have no address
+    if (b->n_seqs > 0 && (!b->row_off || !b->kv_len || (!b->pages && b->ldp > 0) || !al4(b->row_off) ||
+                          !al4(b->kv_len) || !al4(b->pages)))
         return LORA_E_INVALID;
-    if (b->n_groups > 0 && (!b->group_off || !b->prefix_len || !b->prefix_pages || !al4(b->group_off) ||
-                            !al4(b->prefix_len) || !al4(b->prefix_pages)))
+    if (b->n_groups > 0 && (!b->group_off || !b->prefix_len || (!b->prefix_pages && b->ldpp > 0) ||
+                            !al4(b->group_off) || !al4(b->prefix_len) || !al4(b->prefix_pages)))
         return LORA_E_INVALID;
     if (b->n_rows > kMost || b->n_seqs > kMost || b->max_kv_len > kMost || b->max_prefix_len > kMost || b->ldp > kMost ||
         b->ldpp > kMost)

@@ -557,3 +557,20 @@ def test_one_workspace_for_a_shrinking_batch():
         for window in (0, 900):
             attend(case(n, 42 + n), window, 3 if window else 0, what=f"{n} decode rows and a prompt", ws=whole[:need])
             assert bool((whole[need:] == 0xA5).all())
+
+
+def test_tables_without_columns():
+    """All prefixes empty, or all sequences: a page table of no columns."""
+    b = binding()
+    c = Case([1, 20, 1], [30, 40, 9], 8, 2, 64, BF, prefix=[0, 0], group_off=[0, 2, 3], table_pad=0, seed=43)
+    assert c.batch(b).tensors[5].shape == (2, 0)
+    attend(c, what="empty prefixes")
+    attend(c, 7, 2, what="empty prefixes, window")
+    c = Case([1, 20, 0], [0, 0, 0], 8, 2, 64, BF, table_pad=0, seed=44)
+    assert c.batch(b).tensors[2].shape == (3, 0)
+    attend(c, what="no tokens")
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    k = torch.randn((21, 128), device=DEV).to(BF)
+    out = b.lora_kv_append(c.cache(b), c.batch(b), c.q.to(DEV), k, k, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 1 and bool((out == 0).all())

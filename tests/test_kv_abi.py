@@ -176,3 +176,20 @@ def test_workspace_serves_a_shrinking_server():
         batch.n_rows = batch.max_rows = n
         sizes.append(workspace(b, cache, batch, 32))
     assert sizes == sorted(sizes, reverse=True), sizes
+
+
+def test_tables_without_columns():
+    """A page table of no columns has no address: its sequences or prefixes have no tokens."""
+    b, cache, batch, rope = structs()
+    batch.pages, batch.ldp = None, 0
+    n = workspace(b, cache, batch, 4)
+    assert attn(b, cache, batch, ws=None, scale=0.0) == b.LORA_E_INVALID
+    if n:
+        assert attn(b, cache, batch, ws=None) == b.LORA_E_WORKSPACE
+    batch.pages, batch.ldp = FAKE, 4
+    batch.group_off = batch.prefix_len = FAKE
+    batch.prefix_pages, batch.n_groups, batch.ldpp, batch.max_prefix_len, batch.max_group_rows = None, 1, 0, 0, 5
+    assert workspace(b, cache, batch, 4) > 0
+    assert attn(b, cache, batch, fn="lora_attn_prefix", ws=None) == b.LORA_E_WORKSPACE
+    batch.ldpp = 1
+    assert attn(b, cache, batch, fn="lora_attn_prefix", ws=None) == b.LORA_E_INVALID
