@@ -18,7 +18,7 @@ bool dtype_ok(const lora_dtype_t& d) {
 int elem_bytes(lora_dtype_t d) { return d == LORA_BF16 ? 2 : 4; }
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool al4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
-bool ld16(int64_t ld, int eb) { return (ld * eb) % 16 == 0; }
+bool ld16(int64_t ld, int eb) { return ld % (16 / eb) == 0; }
 lora_status_t dev_status(hipError_t e) { return e == hipSuccess ? LORA_OK : LORA_E_DEVICE; }
 
 constexpr int64_t kMost = (int64_t)1 << 30;   // rows, lengths, columns and table widths
@@ -33,7 +33,7 @@ lora_status_t check_cache(const lora_kv_cache_t* c, KvDev& C) {
     if (!al16(c->k) || !al16(c->v) || !ld16(c->page_stride, eb) || !ld16(c->token_stride, eb) ||
         !ld16(c->head_stride, eb))
         return LORA_E_UNSUPPORTED;
-    if (c->token_stride * c->page_size >= kMost) return LORA_E_UNSUPPORTED;   // offsets in a page are 32-bit
+    if (c->token_stride >= kMost / c->page_size) return LORA_E_UNSUPPORTED;   // offsets in a page are 32-bit
     C.k = c->k;
     C.v = c->v;
     C.page_stride = c->page_stride;

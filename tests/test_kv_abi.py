@@ -193,3 +193,13 @@ def test_tables_without_columns():
     assert attn(b, cache, batch, fn="lora_attn_prefix", ws=None) == b.LORA_E_WORKSPACE
     batch.ldpp = 1
     assert attn(b, cache, batch, fn="lora_attn_prefix", ws=None) == b.LORA_E_INVALID
+
+
+@pytest.mark.parametrize("stride", [1 << 26, 1 << 60, (1 << 62) + 64])
+def test_token_strides_past_a_page(stride):
+    """Offsets in a page are 32-bit; a stride whose product with the page wraps around is no smaller."""
+    b, cache, batch, _ = structs()
+    cache.token_stride = stride
+    n = ctypes.c_size_t()
+    got = b.library().lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), 4, ctypes.byref(n))
+    assert got == b.LORA_E_UNSUPPORTED
