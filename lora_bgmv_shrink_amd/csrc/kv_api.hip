@@ -85,7 +85,8 @@ lora_status_t make_plan(const lora_kv_cache_t* cache, const lora_kv_batch_t* bat
     if (st != LORA_OK) return st;
     if (n_q_heads <= 0 || n_q_heads % cache->n_kv_heads != 0 || window < 0 || n_sink < 0) return LORA_E_INVALID;
     if (groups != (batch->n_groups > 0)) return LORA_E_INVALID;
-    if ((int64_t)batch->n_rows * n_q_heads > kMost || (int64_t)batch->n_seqs * cache->n_kv_heads > kMost)
+    if ((int64_t)batch->n_rows * n_q_heads > kMost || (int64_t)batch->n_seqs * cache->n_kv_heads > kMost ||
+        (int64_t)batch->n_groups * cache->n_kv_heads > kMost)
         return LORA_E_UNSUPPORTED;
     P.a.n_q_heads = n_q_heads;
     P.a.share = n_q_heads / cache->n_kv_heads;

@@ -203,3 +203,18 @@ def test_token_strides_past_a_page(stride):
     n = ctypes.c_size_t()
     got = b.library().lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), 4, ctypes.byref(n))
     assert got == b.LORA_E_UNSUPPORTED
+
+
+def test_more_groups_than_launches_hold():
+    """Groups times key heads is a count of workgroups, as sequences times key heads is."""
+    b, cache, batch, _ = structs()
+    cache.n_kv_heads = 8
+    batch.group_off = batch.prefix_len = batch.prefix_pages = FAKE
+    batch.ldpp, batch.max_prefix_len, batch.max_group_rows = 4, 60, 5
+    n = ctypes.c_size_t()
+    for n_groups in ((1 << 27) + 1, 1 << 28, 1 << 30, 2 ** 31 - 1):
+        batch.n_groups = n_groups
+        got = b.library().lora_attn_workspace(ctypes.addressof(cache), ctypes.addressof(batch), 8, ctypes.byref(n))
+        assert got == b.LORA_E_UNSUPPORTED, n_groups
+    batch.n_groups = 1 << 20
+    assert workspace(b, cache, batch, 8) > 0
