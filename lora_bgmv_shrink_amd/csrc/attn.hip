@@ -102,6 +102,9 @@ __device__ __forceinline__ float max_of(float a, float b) {
 // is raised by a score that exceeds it by more; such a weight is noticed in the
 // sum of a lane's weights.
 constexpr float kSlackLog2 = 20.f, kSlack = 1048576.f;
+// as a raw score; finite where c is next to nothing, so that a first score
+// still exceeds -infinity by more
+__device__ __forceinline__ float slack_of(float c) { return fminf(kSlackLog2 / c, 3.402823466e38f); }
 
 // A staged tile of keys or values: rows of D elements as they lie, 16-byte
 // pieces permuted inside a row (or a pair of rows when a row is 128 bytes) so
@@ -649,7 +652,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
     uint8_t* mine_at = stage + wave * WB;   // keys, and then values in their place
     const float c = a.scale * kLog2e;
     const float kInf = __builtin_inff();
-    const float slack = kSlackLog2 / c;   // as a raw score
+    const float slack = slack_of(c);
     // this lane's places in its stage: of the pieces it stores, of its operands
     const int kst = TL::k_at(lane / TL::LPR, lane % TL::LPR), vst = TL::v_at(lane / TL::LPR, lane % TL::LPR);
     const int kop = TL::k_at(l16, TL::piece_of(g4 * 8)), vop = TL::v_base(4 * g4, 0, l16);
@@ -984,7 +987,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
     const int n_prob = problems(a, kind);
     const float c = a.scale * kLog2e;
     const float kInf = __builtin_inff();
-    const float slack = kSlackLog2 / c;   // as a raw score
+    const float slack = slack_of(c);
     // this lane's operands in a staged tile of keys and of values
     const int kop = TL::k_at(l32, TL::piece_of(h2 * 8)), vop = TL::v_base(4 * h2, d16 * 16, l16);
 

@@ -574,3 +574,22 @@ def test_tables_without_columns():
     out = b.lora_kv_append(c.cache(b), c.batch(b), c.q.to(DEV), k, k, status=status)
     torch.cuda.synchronize()
     assert int(status.item()) == 1 and bool((out == 0).all())
+
+
+# a few columns in whole heads and in shares, the tiled form, its wide tiles
+ROWS_AND_TOKENS = [([1], [300]), ([1, 1], [1500, 40]), ([300], [700]), ([1100], [1100])]
+
+
+@pytest.mark.parametrize("case", range(len(ROWS_AND_TOKENS)))
+@pytest.mark.parametrize("prefix", [None, [90]], ids=str)
+@pytest.mark.parametrize("scale", [1e-36, 3e-38, 1e-40])
+def test_scale_near_zero(case, prefix, scale):
+    """Scores of next to nothing: every visible token weighs the same."""
+    b = binding()
+    nq, ln = ROWS_AND_TOKENS[case]
+    c = Case(nq, ln, 64, 8, 64, F32, page=64, prefix=prefix, group_off=prefix and [0, len(nq)], seed=45)
+    say(f"scale {scale}: rows {nq} tokens {ln} prefix {prefix}")
+    lse = torch.empty((c.n_rows, c.hq), device=DEV)
+    fn = b.lora_attn_prefix if prefix else b.lora_attn_paged
+    o = fn(c.cache(b), c.batch(b), c.q.to(DEV), scale, lse=lse)
+    check(c, o, lse, c.reference(scale), "scale near zero")
