@@ -102,6 +102,12 @@ __device__ __forceinline__ float max_of(float a, float b) {
 // is raised by a score that exceeds it by more; such a weight is noticed in the
 // sum of a lane's weights.
 constexpr float kSlackLog2 = 20.f, kSlack = 1048576.f;
+// A weight is exp2((s - m) c).  The tiled form takes it as s c - m c, one
+// operation with m c rounded before; all weights of a column carry that
+// rounding alike and it drops out, unless m c is so large that 2 to its
+// rounding is not near 1 (and for 2^31 no number).  From 2^20 on, where a
+// score in fp32 is known to 2^-4 at best, the difference is taken first.
+constexpr float kLargeLog2 = 1048576.f;
 // as a raw score; finite where c is next to nothing, so that a first score
 // still exceeds -infinity by more
 __device__ __forceinline__ float slack_of(float c) { return fminf(kSlackLog2 / c, 3.402823466e38f); }
@@ -774,12 +780,12 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
                 for (int t = 0; t < D / 16; ++t) acc[t] *= f;
                 if (up) m = top;
             }
-            const float mc = m == -kInf ? 0.f : m * c;
+            const float ref = m == -kInf ? 0.f : m;
             f32x8_t w;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                w[r] = exp2_fast(s[0][r] * c - mc);
-                w[4 + r] = exp2_fast(s[1][r] * c - mc);
+                w[r] = exp2_fast((s[0][r] - ref) * c);
+                w[4 + r] = exp2_fast((s[1][r] - ref) * c);
             }
             l += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
             const typename O::frag pf = O::round(w);
@@ -896,10 +902,10 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
                 mw[w] = all[w * WF + 16 * OP + col];
                 M = fmaxf(M, mw[w]);
             }
-            const float Mc = M == -kInf ? 0.f : M * c;
+            const float ref = M == -kInf ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                mw[w] = exp2_fast(mw[w] * c - Mc);
+                mw[w] = exp2_fast((mw[w] - ref) * c);
                 sum += mw[w] * all[w * WF + 16 * OP + 16 + col];
             }
 #pragma unroll
@@ -1169,12 +1175,14 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
                 for (int ks = 0; ks < D / 16; ++ks)
                     w[kb] = O::mma32(TL::k_frag(sk + kb * 32 * TL::RB, ka ^ (TL::piece_of(ks * 16) << 4)), qf[ks], w[kb]);
             };
-            auto weights = [&](auto kb) __attribute__((always_inline)) {
+            auto weights = [&](auto kb, auto LARGE) __attribute__((always_inline)) {
                 const float mc = m == -kInf ? 0.f : m * c;
+                const bool large = LARGE && !(fabsf(mc) < kLargeLog2);
+                const float ref = large ? m : 0.f, rest = large ? 0.f : mc;
                 float part[4];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    w[kb][r] = exp2_fast(w[kb][r] * c - mc);
+                    w[kb][r] = exp2_fast(LARGE ? (w[kb][r] - ref) * c - rest : w[kb][r] * c - mc);
                     part[r & 3] = r < 4 ? w[kb][r] : part[r & 3] + w[kb][r];
                 }
                 sum[kb] = (part[0] + part[1]) + (part[2] + part[3]);
@@ -1188,20 +1196,20 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
             };
             constexpr Int<0> h0{};
             constexpr Int<1> h1{};
-            // Every key seen and every column with a reference: no branch
-            // until the weights are there.
-            bool done = all_see && !__ballot(m == -kInf);
+            // Every key seen and every column with a reference that is not
+            // large: no branch until the weights are there.
+            bool done = all_see && !__ballot(!(fabsf(m * c) < kLargeLog2));
             if (done) {
                 scores(h0);
                 sched_mix<T, 4, D / 16, 1, 0, 0>();
                 load(Q1, Q2, place, buf ^ 1);
                 scores(h1);
-                weights(h0);
+                weights(h0, h0);
                 sched_mix<T, 4, D / 16, 1, 4, 2>();
                 stay(pf[0][0]);
                 stay(pf[0][1]);
                 load(Q2, Q3, place, buf ^ 1);
-                weights(h1);
+                weights(h1, h0);
                 load(Q3, NL, place, buf ^ 1);
                 done = !__ballot(fmaxf(sum[0], sum[1]) > kSlack);
             } else {
@@ -1232,8 +1240,8 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
                 l *= f;
 #pragma unroll
                 for (int t = 0; t < D / 32; ++t) acc[t] *= f;
-                weights(h0);
-                weights(h1);
+                weights(h0, h1);
+                weights(h1, h1);
             }
             l += sum[0] + sum[1];
 
@@ -1460,9 +1468,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int by_row, int r
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
             const float m_new = fmaxf(M, top);
-            const float mc = m_new == -kInf ? 0.f : m_new * c;
-            const float f = exp2_fast(M * c - mc);
-            const float w = exp2_fast(x.x * c - mc);
+            const float ref = m_new == -kInf ? 0.f : m_new;
+            const float f = exp2_fast((M - ref) * c);
+            const float w = exp2_fast((x.x - ref) * c);
             float sum = sl < here ? w * x.y : 0.f;
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d, 64);

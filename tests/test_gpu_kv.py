@@ -593,3 +593,51 @@ def test_scale_near_zero(case, prefix, scale):
     fn = b.lora_attn_prefix if prefix else b.lora_attn_paged
     o = fn(c.cache(b), c.batch(b), c.q.to(DEV), scale, lse=lse)
     check(c, o, lse, c.reference(scale), "scale near zero")
+
+
+@pytest.mark.parametrize("case", range(len(ROWS_AND_TOKENS)))
+@pytest.mark.parametrize("prefix", [None, [90]], ids=str)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("factor", [1e3, 1e4, 3e4, 1e6, 1e8])
+def test_scores_without_bound(case, prefix, dtype, factor):
+    """Scores up to 1e18: a row is the value of its highest score.
+
+    Rows count whose two highest scores are further apart than fp32 sums of 64 products can move them, 64 * 2^-24 of
+    |q| |k| each, and than the softmax has weight for (40).  Their o is one value times a weight over itself: in bf16
+    the weight and o are rounded, 2^-8 each, in fp32 2^-22 covers it.  lse is the score.
+    """
+    b = binding()
+    nq, ln = ROWS_AND_TOKENS[case]
+    d, hq, hkv, scale = 64, 64, 8, 0.125
+    c = Case(nq, ln, hq, hkv, d, dtype, page=64, prefix=prefix, group_off=prefix and [0, len(nq)], seed=46)
+    c.q = (c.q.float() * factor).to(dtype)
+    for k, pages in [(x[0], p) for x, p in zip(c.own + c.pre, c.pages + c.prefix_pages)]:
+        k *= factor
+        for t in range(0, len(k), c.page):
+            m = min(c.page, len(k) - t)
+            c.cpu_k[pages[t // c.page], :m] = k[t:t + m].float()
+    say(f"scores without bound: factor {factor} rows {nq} tokens {ln} prefix {prefix} {dtype}")
+    lse = torch.empty((c.n_rows, hq), device=DEV)
+    fn = b.lora_attn_prefix if prefix else b.lora_attn_paged
+    o = fn(c.cache(b), c.batch(b), c.q.to(DEV), scale, lse=lse)
+    torch.cuda.synchronize()
+    o, lse = o.double().cpu().view(-1, hq, d), lse.double().cpu()
+    q, row, counted, rows = c.q.double().view(-1, hq, d), 0, 0, 0
+    for s, n in enumerate(nq):
+        k, v = (torch.cat((c.pre[0][i], c.own[s][i])) if prefix else c.own[s][i] for i in (0, 1))
+        k, v = k.double(), v.double()
+        hidden = torch.arange(len(k)) > torch.arange(len(k) - n, len(k))[:, None]
+        for h in range(hq):
+            qh, kh, vh = q[row:row + n, h], k[:, h // (hq // hkv)], v[:, h // (hq // hkv)]
+            x = (torch.matmul(qh, kh.t()) * scale).masked_fill(hidden, -math.inf)
+            top, at = x.topk(min(2, len(k)), -1)
+            moved = 2 * 64 * 2.0 ** -24 * scale * qh.norm(dim=-1) * kh.norm(dim=-1).max()
+            far = top[:, 0] - top[:, -1] > moved + 40
+            counted, rows = counted + int(far.sum()), rows + n
+            want, got = vh[at[:, 0]][far], o[row:row + n, h][far]
+            bound = (2.0 ** -7 if dtype == BF else 2.0 ** -22) * want.abs() + 1e-30
+            assert bool(((got - want).abs() <= bound).all()), (s, h)
+            assert bool(((lse[row:row + n, h] - top[:, 0]).abs() <= moved + 1e-6 * top[:, 0].abs())[far].all()), (s, h)
+        row += n
+    say(f"  {counted} of {rows} rows and heads")
+    assert counted > 0.9 * rows
