@@ -1604,15 +1604,26 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
         if (a.share <= ATTN_FEW_COLS) {
             const int64_t units = ceil_div(reach, ATTN_FEW_KEYS);
             const int64_t heads = (int64_t)n_prob[k] * hkv;
-            // Whole (problem, head) pairs per workgroup where that fills the
-            // card and no pair is much longer than the rest can be (16 units;
-            // with thousands of pairs the hardware's own order evens them
-            // out): 32 requests of up to 2048 tokens 32 us, in shares 45; 256
-            // with a window of 1024 180 us, in shares 220.  And where there
-            // is little to share (4 units).  Otherwise equal shares: 8
-            // requests of 16k to 60k tokens on 8 heads would be 64 pairs.
+            // Whole (problem, head) pairs per workgroup, or equal shares of
+            // all units.  A pair's chain takes 1.7 us a unit, whatever the
+            // others do; shares cost the join and their own ends, some 12
+            // us beyond the reads.  So pairs up to 16 units where there are
+            // 8 pairs a unit, and up to 4 units always (us, whole pairs /
+            // shares, lengths spread up to the longest, 8 key heads of 128):
+            //     requests    640 tokens   1024         2048        4096
+            //     1           12 / 14      17 / 14      27 / 16
+            //     8           13 / 17      17 / 18      28 / 25
+            //     16          13 / 17      18 / 25      28 / 31
+            //     31          13 / 24      18 / 31      31 / 44
+            //     32          13 / 25      18 / 30      30 / 42     58 / 66
+            //     64          21 / 36      27 / 45      56 / 69     104 / 111
+            // One request of 2048 among 31 short ones: 27 / 19; of 4096, 49 /
+            // 23, which is why longer ones are shared though even lengths
+            // would gain (32 of 4096: 83 / 93).  With thousands of pairs the
+            // hardware's own order evens them out (512 of up to 8000: 1381 /
+            // 1404), and there the shares' table would grow.
             auto direct = [](int64_t u, int64_t pairs) {
-                return u <= 4 || (pairs >= 256 && u <= 16) || pairs >= 4096;
+                return u <= 4 || (u <= 16 && pairs >= 8 * u) || pairs >= 4096;
             };
             W.few = direct(units, heads) ? 1 : 2;
             W.few_grid = W.few == 1 ? n_prob[k] * hkv : ATTN_FEW_WGS;

@@ -84,12 +84,28 @@ int main() {
 """
 
 
-def test_plans_fit_their_workspace():
+RULE = r"""
+int main() {
+    // requests of one row and up to so many tokens on 8 key heads: whole heads per workgroup (1) or shares (2)
+    const int rows[][3] = {{1, 512, 1}, {1, 1024, 2}, {8, 1024, 1}, {8, 2048, 2}, {16, 2048, 1}, {31, 2048, 1}, {32, 2048, 1},
+                           {33, 2048, 1}, {32, 4096, 2}, {512, 8000, 1}};
+    for (const auto& r : rows) {
+        const int v[7] = {r[0], r[0], 1, r[1], 0, 0, 0};
+        const AttnPlan P = plan(32, 8, 128, 2, v, 0, 0);
+        std::printf("%d requests of %d tokens: %d\n", r[0], r[1], P.a.part[0].few);
+        if (P.a.part[0].few != r[2]) return 1;
+    }
+    return 0;
+}
+"""
+
+
+def run(main):
+    code = HARNESS[:HARNESS.index("int main()")] + main
     with tempfile.TemporaryDirectory() as d:
-        src, exe = os.path.join(d, "plan.hip"), os.path.join(d, "plan")
+        src, obj, exe = (os.path.join(d, n) for n in ("plan.hip", "plan.o", "plan"))
         with open(src, "w") as f:
-            f.write("#include <algorithm>\n#include <cstring>\n" + HARNESS)
-        obj = os.path.join(d, "plan.o")
+            f.write("#include <algorithm>\n#include <cstring>\n" + code)
         lib = ["-Wl,-rpath," + os.path.dirname(hb.LIB_PATH)]
         for cmd in ([hb.HIPCC, *hb.FLAGS, "-I", hb.CSRC, "-c", src, "-o", obj],
                     [hb.HIPCC, obj, hb.LIB_PATH, *lib, "-o", exe]):
@@ -98,3 +114,11 @@ def test_plans_fit_their_workspace():
         r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
         print(r.stdout)
         assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_plans_fit_their_workspace():
+    run(HARNESS[HARNESS.index("int main()"):])
+
+
+def test_one_request_less_keeps_the_form():
+    run(RULE)
