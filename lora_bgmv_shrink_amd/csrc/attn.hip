@@ -721,6 +721,14 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
             int seq_rows;
             if (there) col_pos = kind == 0 ? P.pos0 + j : a.window > 0 ? row_position(a, P.r0 + j, seq_rows) : P.pos1;
         }
+        // the least position of the columns, from which a window reaches back
+        int lo_pos = P.pos0;
+        if (kind == 1 && a.window > 0) {
+            lo_pos = l16 < P.nr * a.share ? col_pos : 0x7fffffff;
+#pragma unroll
+            for (int x = 1; x < 16; x <<= 1) lo_pos = min(lo_pos, __shfl_xor(lo_pos, x, 64));
+            lo_pos = __builtin_amdgcn_readfirstlane(lo_pos);
+        }
 
         // page number of key `lane` of the wave's unit x (lanes 0 .. 31), -1: none
         auto load_id = [&](int x) __attribute__((always_inline)) {
@@ -735,7 +743,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
             const int key = base_of(x) + lane, at = P.key0 + key;
             const bool page_ok = id >= 0 && id < a.C.n_pages;
             bool seen = lane < KW && key < P.len && at <= P.pos1;
-            if (a.window > 0) seen = seen && (at > P.pos0 - a.window || at < a.n_sink);
+            if (a.window > 0) seen = seen && (at > lo_pos - a.window || at < a.n_sink);
             if (seen && !page_ok && a.status) flag_bad_id(a.status);
             place = place_of(a, page_ok ? id : 0, key, h);
             return (uint32_t)__ballot(seen && page_ok);
@@ -824,9 +832,8 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
         // rows do not see (0 times them is NaN) are looked for in the units
         // that rows see in part; where there are some (the answer) the walk is
         // made again with ODD, which leaves them out of the product and adds
-        // them to the columns that see them.  One row of a sequence sees just
-        // what `bits` says; one row of a group may sit any number of tokens
-        // behind the prefix, past keys that the least position still sees.
+        // them to the columns that see them.  One row sees just what `bits`
+        // says.
         auto walk = [&](auto ODD) __attribute__((always_inline)) {
             m = -kInf;
             l = 0.f;
@@ -854,7 +861,7 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
                     if (!all_see) {
                         asm volatile("");
                         hide_rows<NL>(rv, bits_x, here(lane) / TL::LPR, RPL);
-                        if (!ODD && (P.nr > 1 || kind == 1)) {
+                        if (!ODD && P.nr > 1) {
 #pragma unroll
                             for (int j = 0; j < NL; ++j) odd |= odd_piece<T>(rv[j]);
                         }
@@ -1026,7 +1033,8 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
 
     // the workgroup's rows, its key tiles and this split's run of them
     const int j_lo = ct * TC / a.share, j_hi = min(P.nr - 1, (ct * TC + TC - 1) / a.share);
-    const int wg_lo = kind == 0 ? lowest(P, j_lo) : P.pos0, wg_hi = kind == 0 ? P.pos0 + j_hi : P.pos1;
+    int wg_lo = kind == 0 ? lowest(P, j_lo) : P.pos0;
+    const int wg_hi = kind == 0 ? P.pos0 + j_hi : P.pos1;
     const Walk R = walk_of<KB>(a, F, P, kind == 0 ? P.pos0 + j_lo : P.pos0, wg_hi);
     const int i0 = split * W.spl, i1 = min(R.n(), i0 + W.spl);
     if (split > 0 && i0 >= R.n()) return;
@@ -1057,6 +1065,17 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
         there = (int64_t)seq_rows * a.share <= ATTN_FEW_COLS;   // the others walk the prefix themselves
     }
     if (kind == 1 && !a.decode && !__syncthreads_or(there)) return;
+    if (kind == 1 && a.window > 0) {   // the least position that a window reaches back from
+        int lo = there ? col_pos : 0x7fffffff;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) lo = min(lo, __shfl_xor(lo, x, 64));
+        if (lane == 0) sh[wave] = lo;
+        __syncthreads();
+        wg_lo = sh[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) wg_lo = min(wg_lo, sh[w]);
+        wg_lo = __builtin_amdgcn_readfirstlane(wg_lo);
+    }
     const bool wave_there = __ballot(there) != 0;
     // least and largest position of the wave's columns
     const int wv_lo = kind == 0 ? lowest(P, (ct * TC + wave * 32) / a.share) : P.pos0;

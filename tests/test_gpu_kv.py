@@ -641,3 +641,24 @@ def test_scores_without_bound(case, prefix, dtype, factor):
         row += n
     say(f"  {counted} of {rows} rows and heads")
     assert counted > 0.9 * rows
+
+
+@pytest.mark.parametrize("rows", [1, 2, 30])
+def test_pages_behind_every_window(rows):
+    """Prefix pages that every row's window has left may have any number: status stays 0."""
+    b = binding()
+    n, own, window = 200, 40, 50      # positions 239 on: tokens 190 on are seen
+    c = Case([1] * rows, [own + i for i in range(rows)], 8, 2, 64, BF, page=16, prefix=[n], group_off=[0, rows], seed=47)
+    q, status = c.q.to(DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    for sinks in (0, 3):
+        want = attend(c, window, sinks, what="windows past a prefix's pages")
+        for page, needed in ((10, False), (9, False), (1, False), (12, True), (0, sinks > 0)):
+            d = Case([1] * rows, c.kv_len, 8, 2, 64, BF, page=16, prefix=[n], group_off=[0, rows], seed=47)
+            d.prefix_pages[0][page] = -1
+            status.zero_()
+            say(f"rows {rows} sinks {sinks} page {page}")
+            o = b.lora_attn_prefix(c.cache(b), d.batch(b), q, 0.125, window=window, n_sink=sinks, status=status)
+            torch.cuda.synchronize()
+            assert int(status.item()) == int(needed), (page, sinks)
+            if not needed:
+                assert torch.equal(o.double().cpu(), want)
