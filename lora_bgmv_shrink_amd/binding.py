@@ -606,12 +606,12 @@ class Rope:
         self.ref = ctypes.addressof(self.struct)
 
 
-def _heads(t: torch.Tensor, cache: KvCache, rows: int) -> int:
-    d = cache.head_dim
-    assert t.is_cuda and t.get_device() == cache.index, "a tensor of the cache's device"
-    assert t.dim() == 2 and t.stride(1) == 1 and t.shape[0] == rows and t.shape[1] % d == 0, \
-        "expected [n_rows, heads * head_dim], row-major"
-    return t.shape[1] // d
+def _heads(t: torch.Tensor, cache: KvCache, n_rows: int) -> int:
+    assert t.get_device() == cache.index and t.dim() == 2 and t.stride(1) == 1, \
+        "expected a row-major tensor of the cache's device"
+    rows, width = t.shape
+    assert rows == n_rows and width % cache.head_dim == 0, "expected [n_rows, heads * head_dim]"
+    return width // cache.head_dim
 
 
 def _here(t: Optional[torch.Tensor], cache: KvCache, dtype: torch.dtype) -> bool:
