@@ -101,7 +101,7 @@ lora_status_t make_plan(const lora_kv_cache_t* cache, const lora_kv_batch_t* bat
 
 lora_status_t run_attn(const lora_kv_cache_t* cache, const lora_kv_batch_t* batch, const void* q, int64_t ldq,
                        int32_t n_q_heads, float scale, int32_t window, int32_t n_sink, bool groups, void* o,
-                       lora_dtype_t o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws, size_t ws_bytes,
+                       const lora_dtype_t& o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws, size_t ws_bytes,
                        hipStream_t stream) {
     AttnPlan P;
     const lora_status_t st = make_plan(cache, batch, n_q_heads, window, n_sink, groups, P);
