@@ -711,8 +711,8 @@ typedef struct {
  * launch; every element is computed in fp32 and rounded once.
  *   q [n_rows, ldq], k and v [n_rows, ldk / ldv] of `dtype` (heads side by
  *   side, as the projections leave them); q_out [n_rows, ldqo] of the cache's
- *   type, which may be q itself when the types agree.  n_q_heads = 0: keys
- *   and values only.
+ *   type, which may be q itself when the types agree (ldqo = ldq then).
+ *   n_q_heads = 0: keys and values only.
  *   status (device, may be NULL) gets bit 0 set when a row has no place: its
  *   index is negative or past the page table, its page number outside
  *   [0, n_pages), or its position outside the rotary tables.  Nothing is
@@ -731,10 +731,11 @@ lora_status_t lora_kv_append(const lora_kv_cache_t* cache, const lora_kv_batch_t
  * k < n_sink (a sliding window whose first tokens stay visible).  A row that
  * sees nothing gets o = 0 and lse = -infinity.  What a row does not see has
  * no effect on it, infinities and NaN in the pages included.
- *   q [n_rows, ldq] of the cache's type; o [n_rows, ldo] of o_dtype; lse
- *   [n_rows, n_q_heads] fp32, may be NULL; scale > 0.
+ *   q [n_rows, ldq] of the cache's type; o [n_rows, ldo] of o_dtype, apart
+ *   from q; lse [n_rows, n_q_heads] fp32, may be NULL; scale > 0.
  *   Scores, softmax statistics and sums are fp32; the weights are rounded to
- *   the cache's type before the product with V, and o once at the end.
+ *   the cache's type before the product with V, and o once at the end (so an
+ *   fp32 o of a bf16 cache still has the weights' rounding, 2^-8 of each).
  *   status (device, may be NULL) gets bit 0 set when a page number that some
  *   row needs is outside [0, n_pages); its tokens are then not seen.
  * Results do not depend on timing.  lora_attn_paged takes a batch without

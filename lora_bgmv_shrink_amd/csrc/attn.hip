@@ -622,18 +622,21 @@ __device__ __forceinline__ uint64_t sees(const AttnArgs& a, int col_pos, int lo,
 //
 // A work unit is 128 keys of one (problem, key head); each of the four waves
 // takes 32 of them through LDS of its own (no barrier; values take the keys'
-// place once those are multiplied, so that three workgroups fit a CU), with
-// the next unit's pieces in flight in registers and the unit after's page
-// numbers before them.  Shared form (few = 2): the units of all problems are
-// dealt to the workgroups in equal runs, whatever the lengths; a run's first
-// and last (problem, head) may be partial and go to slots that the join adds.
-// Otherwise a workgroup takes one (problem, head) whole.
+// place once those are multiplied), with the next unit's pieces in flight in
+// registers and the unit after's page numbers before them.  At 128 dimensions
+// that is 253 registers a lane, two workgroups a CU (and 149 scalar registers
+// kept in vector lanes); at 64, three.  Shared form (few = 2): the units of
+// all problems are dealt to the workgroups in equal runs, whatever the
+// lengths; a run's first and last (problem, head) may be partial and go to
+// slots that the join adds.  Otherwise a workgroup takes one (problem, head)
+// whole.
 //
 // bf16, 8 key heads of 128, 8 sequences of 16 k to 60 k tokens: 189 us, 1.14
 // GB, 6.0 TB/s (a plain read of this shape: 6.5); 256 sequences that see 1024
-// tokens and 4 sinks: 180 us, 5.6 TB/s; 32 sequences of up to 2048 tokens: 31
-// us, 4.3 TB/s, of which some 6 us are a piece's beginning (its problem, its
-// q, its first keys: loads that depend on one another) and its end.
+// tokens and 4 sinks: 180 us, 0.94 GB seen and, in whole units, 1.14 GB read,
+// 6.3 TB/s; 32 sequences of up to 2048 tokens: 32 us, 4.2 TB/s, of which some
+// 6 us are a piece's beginning (its problem, its q, its first keys: loads that
+// depend on one another) and its end.
 template <typename T, int D>
 struct FewStage {   // LDS of a wave: 32 keys, or 16 columns of O and their statistics
     static constexpr int KEYS = ATTN_FEW_KEYS / 4 * Tile<T, D>::RB, OUT = 16 * (D + 4) * 4 + 128;
@@ -975,12 +978,18 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
 // so that the columns of one head meet in one XCD's L2, and later column
 // tiles (more keys under the causal mask) first.
 //
-// bf16, 32 heads on 8 of 128, a prompt of 8192 tokens: 580 us, 948 TFLOP/s of
-// the 1232 that a large matrix product reaches; 64 heads on 8, 2048 rows that
-// see 4096 tokens of 10 k: 169 us, 510 TFLOP/s (256 items of unequal length
-// on 256 CUs).  A tile of 64 keys by 256 columns takes 2.5 us, of them 1.1 at
-// the matrix cores' rate; the rest is LDS reads' latency, the waves' skew at
-// the barrier and the softmax's vector work.
+// bf16, 32 heads on 8 of 128, a prompt of 8192 tokens: 570 us, 965 TFLOP/s of
+// the 1273 that a large matrix product reaches.  A tile of 64 keys by 256
+// columns takes 2.2 us of a CU, of them 0.9 at the matrix cores' peak; the
+// rest is LDS reads' latency, the waves' skew at the barrier and the softmax's
+// vector work.  Beside 16 decode rows, 4 prompt pieces of 512 rows, 64 heads
+// on 8, in windows of 2048 with 4 sinks (8.6e10 flop): 169 us in three
+// launches one after another, this one 136, the few-column form 33, the join
+// 6.  Its 512 items have 2 to 35 tiles and take 49 in a row on 256 CUs (43 if
+// they were even), 2.8 us each: the tiles at the window's ends are masked,
+// their values looked over behind a second barrier, and the sinks cost one
+// tile more.  Over a prefix with a window (kind 1) every tile goes that way,
+// since what a window's row sees is not known from its place in the group.
 //
 // Only rows of up to 256 bytes leave the registers for tiles of 256 columns.
 template <typename T, int D> constexpr bool kWide = sizeof(T) * D <= 256;
@@ -1357,7 +1366,9 @@ void k_attn_tile(AttnArgs a) {
 // tokens): their workgroups alternate, eight by eight so that each kind still
 // goes round the XCDs, and the one's matrix products run beside the other's
 // reads.  256 requests behind eight prefixes of 1000 to 8000 tokens, 64 heads
-// on 8: 226 us with the join, 0.72 GB and 4.9e10 flop.
+// on 8: 226 us with the join, 0.72 GB and 5.0e10 flop (3.4 TB/s: a CU holds two
+// workgroups of either form, so beside a tile half as many reads are in
+// flight as beside another reader).
 template <typename T, int D, bool PAGED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) * D <= 256 ? 2 : 1)))
 void k_attn_both(AttnArgs a) {

@@ -10,7 +10,7 @@
 // for prompts (20304 rows of 64 heads on 8 of 128, bf16: 163 us, 5.1 TB/s, the
 // rate of a plain copy); for one decode step the time is the chain of
 // dependent loads (row's sequence -> its length -> its page -> the store): 32
-// rows of 32 heads on 8, 3.9 us.
+// rows of 32 heads on 8, 4 us.
 #include "kv_internal.hpp"
 
 namespace lora {
