@@ -759,6 +759,119 @@ lora_status_t lora_attn_prefix(const lora_kv_cache_t* cache, const lora_kv_batch
                                lora_dtype_t o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws,
                                size_t ws_bytes, hipStream_t stream);
 
+/* A step's tables made on the device from the rows that each request brings:
+ * pages are taken from a stack of free ones and given back to it, and every
+ * row of the step gets its sequence, adapter, position and place.  What it
+ * writes is what the layer (ids), lora_kv_append and the attention (row_off,
+ * kv_len, pages) read, so a step whose requests change can be a replayed
+ * graph.  Arrays are device.
+ *   new_rows[n_seqs]   rows of sequence s in this step (0: none); below zero:
+ *                      its request is over, its pages go back onto the stack
+ *                      (in the order of the sequences and of their tables)
+ *                      before any is taken, and its length becomes 0;
+ *   adapter[n_seqs]    its adapter, for row_adapter; may be NULL (-1);
+ *   kv_len[n_seqs]     its tokens before the step; kv_len_out: after it, may
+ *                      be kv_len itself;
+ *   pages[n_seqs, ldp] its page table, in and out: entries of new pages are
+ *                      written, no others;
+ *   free_pages[max_free], n_free[1]  the stack, taken from its top, and its
+ *                      height; n_free_out may be n_free itself.  Entries past
+ *                      the new height are left as they are;
+ *   group_off[n_groups + 1], prefix_len[n_groups]  as in lora_kv_batch_t, for
+ *                      row_pos; n_groups = 0: no prefixes.
+ * A sequence gets all of its rows or none.  In the order of the sequences, one
+ * is refused when its tokens would not fit its table (ldp * page_size); when
+ * its rows and those of the sequences before it, other ones that do not fit
+ * their tables left out, are more than max_rows; or when it needs pages and
+ * these and the ones that those sequences need are more than there are.  So
+ * what a refused request asked for is not given to a later one, but a later one
+ * that needs no page is served.
+ * Written:
+ *   row_off[n_seqs + 1]  rows of sequence s: row_off[s] .. row_off[s + 1] - 1
+ *                        (none where it was refused);
+ *   row_seq, row_adapter, row_pos [max_rows]  a row's sequence, adapter and
+ *                        position (its prefix's tokens included);
+ *   row_slot[max_rows]   its place in the cache, page * page_size + token.
+ * Each of the row arrays may be NULL.  Rows from row_off[n_seqs] on get -1 in
+ * all of them, and no place.
+ *   status (may be NULL) gets bit 0 set when a sequence was refused, bit 1
+ *   when more pages came back than the stack holds (the last are dropped).
+ * page_size: a power of two; n_seqs at most 2^20.  Contents that break these
+ * rules give unspecified values, but nothing outside the arrays is read or
+ * written.  One launch for steps of up to 1024 sequences and 4096 rows,
+ * otherwise two.  The workspace (lora_kv_plan_workspace, 16-byte aligned)
+ * needs no zero-filling. */
+typedef struct {
+    const int32_t* new_rows;
+    const int32_t* adapter;
+    const int32_t* kv_len;
+    int32_t* kv_len_out;
+    int32_t* pages;
+    int64_t ldp;
+    int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* n_free_out;
+    const int32_t* group_off;
+    const int32_t* prefix_len;
+    int32_t* row_off;
+    int32_t* row_seq;
+    int32_t* row_adapter;
+    int32_t* row_pos;
+    int64_t* row_slot;
+    int32_t n_seqs, n_groups, page_size, max_free, max_rows;
+} lora_kv_plan_t;
+lora_status_t lora_kv_plan_workspace(const lora_kv_plan_t* plan, size_t* bytes);
+lora_status_t lora_kv_plan(const lora_kv_plan_t* plan, int32_t* status, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* The same cache in 8 bits: a key or value is an e4m3 number (4 bits of
+ * exponent, 3 of fraction, no infinities, largest 448) times a power of two
+ * that the tokens of a block share, for each key head and for keys and values
+ * apart.  Block b of a page holds its tokens b * block_size ..; block_size is
+ * a power of two, at most page_size and 128.  Element (p, t, h, d) of K is
+ *     e4m3(k[p * page_stride + t * token_stride + h * head_stride + d]) *
+ *     k_scale[p * scale_page_stride + (t / block_size) * scale_block_stride + h * scale_head_stride]
+ * and of V alike.  head_dim: 64, 128 or 256.  k and v are 16-byte aligned, and
+ * so are their strides (in bytes, as in elements); the scales' are free.
+ * Of a scale only the exponent is looked at: it is a power of two from 2^-100
+ * to 2^100 (what lora_kv_append_q8 writes; others count as the nearer end). */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t page_stride, token_stride, head_stride;
+    int64_t scale_page_stride, scale_block_stride, scale_head_stride;
+    int32_t n_pages, page_size, block_size, n_kv_heads, head_dim;
+} lora_kv_cache_q8_t;
+
+/* lora_kv_append into a cache in 8 bits (arguments, status and checks as
+ * there; q_out is bf16).  Keys are rotated in 64 bits, so that each element is
+ * rounded once, from its exact value.  A block's scale is the least power of
+ * two under which the largest of its tokens' elements is at most 448; where
+ * the block held tokens of the sequence before, no less than it was, and if it
+ * grows those tokens are rounded again to the new one (which drops bits only
+ * of values that fall below 2^-6 of the scale).  Infinities and NaN become NaN
+ * and do not count for the scale; values past 448 * 2^100 become that. */
+lora_status_t lora_kv_append_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, const lora_rope_t* rope,
+                                lora_dtype_t dtype, const void* q, int64_t ldq, int32_t n_q_heads, const void* k,
+                                int64_t ldk, const void* v, int64_t ldv, void* q_out, int64_t ldqo, int32_t* status,
+                                hipStream_t stream);
+
+/* lora_attn_workspace, lora_attn_paged and lora_attn_prefix over a cache in 8
+ * bits; q is bf16.  Keys and values are widened to bf16, which holds an e4m3
+ * number times a power of two as it is: results are those of a bf16 cache
+ * that holds the same numbers, up to the order of sums. */
+lora_status_t lora_attn_workspace_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, int32_t n_q_heads,
+                                     size_t* bytes);
+lora_status_t lora_attn_paged_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, const void* q,
+                                 int64_t ldq, int32_t n_q_heads, float scale, int32_t window, int32_t n_sink, void* o,
+                                 lora_dtype_t o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+lora_status_t lora_attn_prefix_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, const void* q,
+                                  int64_t ldq, int32_t n_q_heads, float scale, int32_t window, int32_t n_sink, void* o,
+                                  lora_dtype_t o_dtype, int64_t ldo, float* lse, int32_t* status, void* ws,
+                                  size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

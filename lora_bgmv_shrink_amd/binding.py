@@ -50,6 +50,8 @@ EXPORTS = [
     "lora_sched_create", "lora_sched_destroy", "lora_sched_submit", "lora_sched_step", "lora_sched_queued",
     "lora_layer_apply_noalloc", "lora_layer_q4_workspace", "lora_layer_apply_q4",
     "lora_kv_append", "lora_attn_workspace", "lora_attn_paged", "lora_attn_prefix",
+    "lora_kv_plan_workspace", "lora_kv_plan", "lora_kv_append_q8", "lora_attn_workspace_q8", "lora_attn_paged_q8",
+    "lora_attn_prefix_q8",
 ]
 
 
@@ -101,6 +103,21 @@ class KvBatchT(ctypes.Structure):
 class RopeT(ctypes.Structure):
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("ld", ctypes.c_int64),
                 ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class KvCacheQ8T(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+        [(n, ctypes.c_int64) for n in ("page_stride", "token_stride", "head_stride", "scale_page_stride",
+                                       "scale_block_stride", "scale_head_stride")] + \
+        [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "block_size", "n_kv_heads", "head_dim")]
+
+
+class KvPlanT(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("new_rows", "adapter", "kv_len", "kv_len_out", "pages")] + \
+        [("ldp", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("free_pages", "n_free", "n_free_out", "group_off", "prefix_len", "row_off",
+                                        "row_seq", "row_adapter", "row_pos", "row_slot")] + \
+        [(n, ctypes.c_int32) for n in ("n_seqs", "n_groups", "page_size", "max_free", "max_rows")]
 
 
 def _load():
@@ -160,6 +177,12 @@ def _load():
         "lora_attn_workspace": (st, [p, p, i32, p]),
         "lora_attn_paged": (st, [p, p, p, i64, i32, ctypes.c_float, i32, i32, p, st, i64, p, p, p, sz, p]),
         "lora_attn_prefix": (st, [p, p, p, i64, i32, ctypes.c_float, i32, i32, p, st, i64, p, p, p, sz, p]),
+        "lora_kv_plan_workspace": (st, [p, p]),
+        "lora_kv_plan": (st, [p, p, p, sz, p]),
+        "lora_kv_append_q8": (st, [p, p, p, st, p, i64, i32, p, i64, p, i64, p, i64, p, p]),
+        "lora_attn_workspace_q8": (st, [p, p, i32, p]),
+        "lora_attn_paged_q8": (st, [p, p, p, i64, i32, ctypes.c_float, i32, i32, p, st, i64, p, p, p, sz, p]),
+        "lora_attn_prefix_q8": (st, [p, p, p, i64, i32, ctypes.c_float, i32, i32, p, st, i64, p, p, p, sz, p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -554,6 +577,34 @@ class KvCache:
         self.ref = ctypes.addressof(self.struct)
 
 
+class KvCacheQ8:
+    """A paged cache in 8 bits (lora_kv_cache_q8_t): ``k`` and ``v``
+    float8_e4m3fn as in KvCache, ``k_scale`` and ``v_scale`` fp32 seen as
+    [n_pages, page_size / block_size, n_kv_heads] with equal strides; the
+    block size follows from their shape.  Keeps the tensors alive."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        assert k.is_cuda and v.is_cuda and k.dim() == 4 and k.dtype == v.dtype == torch.float8_e4m3fn
+        assert k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1, \
+            "k and v: one shape, equal strides, head_dim contiguous"
+        self.index = k.get_device()
+        for t in (v, k_scale, v_scale):
+            assert t.is_cuda and t.get_device() == self.index, "tensors of one device"
+        assert k_scale.dtype == v_scale.dtype == torch.float32 and k_scale.dim() == 3
+        assert k_scale.shape == v_scale.shape and k_scale.stride() == v_scale.stride(), \
+            "k_scale and v_scale: one shape, equal strides"
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = (int(n) for n in k.shape)
+        blocks = int(k_scale.shape[1])
+        assert k_scale.shape[0] == self.n_pages and k_scale.shape[2] == self.n_kv_heads and blocks > 0 \
+            and self.page_size % blocks == 0, "scales: [n_pages, page_size / block_size, n_kv_heads]"
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        self.block_size, self.dtype = self.page_size // blocks, torch.bfloat16   # of q, and what numbers widen to
+        self.struct = KvCacheQ8T(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0),
+                                 k.stride(1), k.stride(2), k_scale.stride(0), k_scale.stride(1), k_scale.stride(2),
+                                 self.n_pages, self.page_size, self.block_size, self.n_kv_heads, self.head_dim)
+        self.ref = ctypes.addressof(self.struct)
+
+
 class KvBatch:
     """One step's sequences (lora_kv_batch_t): int32 device tensors, and the
     host bounds that size launches and workspaces (of the prefixes too, where
@@ -619,12 +670,9 @@ def _here(t: Optional[torch.Tensor], cache: KvCache, dtype: torch.dtype) -> bool
     return t is None or (t.is_cuda and t.get_device() == cache.index and t.dtype == dtype and t.numel() > 0)
 
 
-def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
-                   rope: Optional[Rope] = None, q_out: Optional[torch.Tensor] = None,
-                   status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
-    """Rotate the rows' q and k, write k and v into their pages and return
-    the rotated q in the cache's type (``q_out``, allocated when not given;
-    None without q)."""
+def _append(fn, where: str, cache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+            rope: Optional[Rope], q_out: Optional[torch.Tensor],
+            status: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     n, d = batch.n_rows, cache.head_dim
     assert batch.index == cache.index and (rope is None or rope.index == cache.index), "tensors of the cache's device"
     assert k.dtype == v.dtype and _heads(k, cache, n) == cache.n_kv_heads == _heads(v, cache, n)
@@ -636,14 +684,29 @@ def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k:
             q_out = torch.empty((n, hq * d), dtype=cache.dtype, device=q.device)
         assert q_out.dtype == cache.dtype and _heads(q_out, cache, n) == hq
     assert _here(status, cache, torch.int32), "status: int32, of the cache's device"
-    st = _lib.lora_kv_append(cache.ref, batch.ref, None if rope is None else rope.ref, _dt(k.dtype),
-                             q.data_ptr() if hq else None, q.stride(0) if hq else 0, hq, k.data_ptr(), k.stride(0),
-                             v.data_ptr(), v.stride(0), q_out.data_ptr() if hq else None,
-                             q_out.stride(0) if hq else 0, None if status is None else status.data_ptr(),
-                             _stream(k.device))
+    st = fn(cache.ref, batch.ref, None if rope is None else rope.ref, _dt(k.dtype), q.data_ptr() if hq else None,
+            q.stride(0) if hq else 0, hq, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+            q_out.data_ptr() if hq else None, q_out.stride(0) if hq else 0,
+            None if status is None else status.data_ptr(), _stream(k.device))
     if st:
-        _check(st, "lora_kv_append")
+        _check(st, where)
     return q_out if hq else None
+
+
+def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                   rope: Optional[Rope] = None, q_out: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Rotate the rows' q and k, write k and v into their pages and return
+    the rotated q in the cache's type (``q_out``, allocated when not given;
+    None without q)."""
+    return _append(_lib.lora_kv_append, "lora_kv_append", cache, batch, q, k, v, rope, q_out, status)
+
+
+def lora_kv_append_q8(cache: KvCacheQ8, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                      rope: Optional[Rope] = None, q_out: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """lora_kv_append into a cache in 8 bits; the rotated q is bf16."""
+    return _append(_lib.lora_kv_append_q8, "lora_kv_append_q8", cache, batch, q, k, v, rope, q_out, status)
 
 
 def lora_attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> int:
@@ -659,7 +722,18 @@ def attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> torch.Tens
     return torch.empty(lora_attn_workspace(cache, batch, n_q_heads), dtype=torch.uint8, device=cache.device)
 
 
-def _attn(fn, where: str, cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: float, window: int, n_sink: int,
+def lora_attn_workspace_q8(cache: KvCacheQ8, batch: KvBatch, n_q_heads: int) -> int:
+    v = ctypes.c_size_t()
+    _check(_lib.lora_attn_workspace_q8(cache.ref, batch.ref, n_q_heads, ctypes.byref(v)), "lora_attn_workspace_q8")
+    return v.value
+
+
+def attn_workspace_q8(cache: KvCacheQ8, batch: KvBatch, n_q_heads: int) -> torch.Tensor:
+    """attn_workspace for a cache in 8 bits."""
+    return torch.empty(lora_attn_workspace_q8(cache, batch, n_q_heads), dtype=torch.uint8, device=cache.device)
+
+
+def _attn(fn, where: str, workspace, cache, batch: KvBatch, q: torch.Tensor, scale: float, window: int, n_sink: int,
           o: Optional[torch.Tensor], o_dtype: Optional[torch.dtype], lse: Optional[torch.Tensor],
           status: Optional[torch.Tensor], ws: Optional[torch.Tensor]) -> torch.Tensor:
     n, d = batch.n_rows, cache.head_dim
@@ -674,7 +748,7 @@ def _attn(fn, where: str, cache: KvCache, batch: KvBatch, q: torch.Tensor, scale
         assert lse.shape == (n, hq) and lse.is_contiguous()
     assert _here(status, cache, torch.int32), "status: int32, of the cache's device"
     if ws is None:
-        ws = attn_workspace(cache, batch, hq)
+        ws = workspace(cache, batch, hq)
     assert ws.is_cuda and ws.get_device() == cache.index and ws.is_contiguous(), "a workspace of the cache's device"
     st = fn(cache.ref, batch.ref, q.data_ptr(), q.stride(0), hq, scale, window, n_sink, o.data_ptr(), _dt(o.dtype),
             o.stride(0), None if lse is None else lse.data_ptr(), None if status is None else status.data_ptr(),
@@ -690,8 +764,8 @@ def lora_attn_paged(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: floa
                     ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of the batch's rows over their pages; ``lse`` [n_rows,
     n_q_heads] fp32 is filled when given."""
-    return _attn(_lib.lora_attn_paged, "lora_attn_paged", cache, batch, q, scale, window, n_sink, o, o_dtype, lse,
-                 status, ws)
+    return _attn(_lib.lora_attn_paged, "lora_attn_paged", attn_workspace, cache, batch, q, scale, window, n_sink, o,
+                 o_dtype, lse, status, ws)
 
 
 def lora_attn_prefix(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0, n_sink: int = 0,
@@ -700,8 +774,94 @@ def lora_attn_prefix(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: flo
                      ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """lora_attn_paged for a batch whose groups of sequences share a prefix,
     which a group's decode rows read once together."""
-    return _attn(_lib.lora_attn_prefix, "lora_attn_prefix", cache, batch, q, scale, window, n_sink, o, o_dtype, lse,
-                 status, ws)
+    return _attn(_lib.lora_attn_prefix, "lora_attn_prefix", attn_workspace, cache, batch, q, scale, window, n_sink, o,
+                 o_dtype, lse, status, ws)
+
+
+def lora_attn_paged_q8(cache: KvCacheQ8, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0,
+                       n_sink: int = 0, o: Optional[torch.Tensor] = None, o_dtype: Optional[torch.dtype] = None,
+                       lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """lora_attn_paged over a cache in 8 bits; q is bf16."""
+    return _attn(_lib.lora_attn_paged_q8, "lora_attn_paged_q8", attn_workspace_q8, cache, batch, q, scale, window,
+                 n_sink, o, o_dtype, lse, status, ws)
+
+
+def lora_attn_prefix_q8(cache: KvCacheQ8, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0,
+                        n_sink: int = 0, o: Optional[torch.Tensor] = None, o_dtype: Optional[torch.dtype] = None,
+                        lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """lora_attn_prefix over a cache in 8 bits; q is bf16."""
+    return _attn(_lib.lora_attn_prefix_q8, "lora_attn_prefix_q8", attn_workspace_q8, cache, batch, q, scale, window,
+                 n_sink, o, o_dtype, lse, status, ws)
+
+
+# --------------------------------------------------------------------------
+# A step's tables
+# --------------------------------------------------------------------------
+
+class KvPlan:
+    """What a server's steps plan with (lora_kv_plan_t): its sequences'
+    lengths ``kv_len`` [n_seqs] and page tables ``pages`` [n_seqs, ldp], the
+    stack ``free_pages`` with its height ``n_free`` [1] (int32 device tensors,
+    all updated in place by every step; ``kv_len_out`` and ``n_free_out``
+    leave the old lengths and height as they are), and the step's tables, which
+    every call writes: ``row_off`` [n_seqs + 1], ``row_seq``, ``row_adapter``,
+    ``row_pos`` [max_rows] int32 and ``row_slot`` [max_rows] int64."""
+
+    def __init__(self, kv_len: torch.Tensor, pages: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
+                 page_size: int, max_rows: int, kv_len_out: Optional[torch.Tensor] = None,
+                 n_free_out: Optional[torch.Tensor] = None, group_off: Optional[torch.Tensor] = None,
+                 prefix_len: Optional[torch.Tensor] = None):
+        kv_len_out = kv_len if kv_len_out is None else kv_len_out
+        n_free_out = n_free if n_free_out is None else n_free_out
+        self.index, dev, n = kv_len.get_device(), kv_len.device, kv_len.numel()
+        for t in (kv_len, pages, free_pages, n_free, kv_len_out, n_free_out, group_off, prefix_len):
+            assert t is None or (t.is_cuda and t.get_device() == self.index and t.dtype == torch.int32
+                                 and t.is_contiguous()), "contiguous int32 tensors of one device"
+        assert kv_len_out.numel() == n and n_free.numel() == n_free_out.numel() == 1
+        assert pages.dim() == 2 and pages.shape[0] == n, "pages: [n_seqs, ldp]"
+        n_groups = 0 if group_off is None else group_off.numel() - 1
+        assert not n_groups or (prefix_len is not None and prefix_len.numel() == n_groups), "groups have prefix_len"
+        self.n_seqs, self.max_rows = n, int(max_rows)
+
+        def rows(length, dtype=torch.int32):
+            return torch.empty(length, dtype=dtype, device=dev)
+
+        self.row_off, self.row_slot = rows(n + 1), rows(self.max_rows, torch.int64)
+        self.row_seq, self.row_adapter, self.row_pos = (rows(self.max_rows) for _ in range(3))
+        self.kv_len, self.pages, self.free_pages, self.n_free = kv_len, pages, free_pages, n_free
+        self.kv_len_out, self.n_free_out, self.group_off, self.prefix_len = kv_len_out, n_free_out, group_off, prefix_len
+        self.struct = KvPlanT(None, None, kv_len.data_ptr(), kv_len_out.data_ptr(), pages.data_ptr(),
+                              int(pages.shape[1]), free_pages.data_ptr(), n_free.data_ptr(), n_free_out.data_ptr(),
+                              group_off.data_ptr() if n_groups else None, prefix_len.data_ptr() if n_groups else None,
+                              self.row_off.data_ptr(), self.row_seq.data_ptr(), self.row_adapter.data_ptr(),
+                              self.row_pos.data_ptr(), self.row_slot.data_ptr(), n, n_groups, int(page_size),
+                              free_pages.numel(), self.max_rows)
+        self.ref = ctypes.addressof(self.struct)
+        self.struct.new_rows = kv_len.data_ptr()   # for the query's checks; a call names its own
+        v = ctypes.c_size_t()
+        _check(_lib.lora_kv_plan_workspace(self.ref, ctypes.byref(v)), "lora_kv_plan_workspace")
+        self.ws = torch.empty(v.value, dtype=torch.uint8, device=dev)
+
+
+def lora_kv_plan(plan: KvPlan, new_rows: torch.Tensor, adapter: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None) -> KvPlan:
+    """One step's tables from the rows ``new_rows`` [n_seqs] that each request
+    brings (below zero: it is over) and their adapters; returns ``plan``, whose
+    tensors are written.  Calls with one plan do not overlap in time."""
+    for t in (new_rows, adapter):
+        assert t is None or (t.is_cuda and t.get_device() == plan.index and t.dtype == torch.int32
+                             and t.is_contiguous() and t.numel() == plan.n_seqs), "int32 [n_seqs] of the plan's device"
+    assert status is None or (status.is_cuda and status.get_device() == plan.index and status.dtype == torch.int32
+                              and status.numel() > 0), "status: int32, of the plan's device"
+    plan.struct.new_rows = new_rows.data_ptr()
+    plan.struct.adapter = None if adapter is None else adapter.data_ptr()
+    st = _lib.lora_kv_plan(plan.ref, None if status is None else status.data_ptr(), plan.ws.data_ptr(),
+                           plan.ws.numel(), _stream(new_rows.device))
+    if st:
+        _check(st, "lora_kv_plan")
+    return plan
 
 
 # --------------------------------------------------------------------------

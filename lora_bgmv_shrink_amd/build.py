@@ -20,7 +20,7 @@ LIB_NAME = "liblora_mi355x.so"
 # sanitizer run's instrumented copy); the default is the in-tree build
 LIB_PATH = os.environ.get("LORA_MI355X_LIB") or os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.hip", "segments.hip", "bgmv.hip", "mfma.hip", "decode.hip", "merge.hip", "cache.hip", "rows.hip", "sched.cpp",
-           "kv.hip", "attn.hip", "kv_api.hip"]
+           "kv.hip", "kv_q8.hip", "kv_plan.hip", "attn.hip", "attn_q8.hip", "kv_api.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -48,6 +48,20 @@ __device__ inline int wave_find_run(const int32_t* __restrict__ off, int n, int 
     return lo;
 }
 
+// What a cache in 8 bits has besides (KvDev's strides are then bytes).
+constexpr int Q8_LEAST = -100, Q8_MOST = 100;   // exponents of a scale
+struct Q8Dev {
+    float* k_scale;
+    float* v_scale;
+    int64_t page_stride, block_stride, head_stride;   // of the scales
+    int32_t block_shift;   // block_size = 1 << block_shift
+    int32_t n_kv_heads;
+    // append: room for a sequence's blocks beyond its rows / block_size, and
+    // all (block, head, K or V) units
+    int32_t per;
+    int64_t units;
+};
+
 struct AppendArgs {
     KvDev C;
     KvBatchDev B;
@@ -64,9 +78,38 @@ struct AppendArgs {
     void* q_out;
     int64_t ldqo;
     int32_t* status;
+    Q8Dev S;
 };
 hipError_t launch_kv_append(const AppendArgs& a, lora_dtype_t in, lora_dtype_t cache, int32_t head_dim,
                             hipStream_t stream);
+// C.n_kv_heads is 0 here (the rows' part is the queries'), S.n_kv_heads is not
+hipError_t launch_kv_append_q8(const AppendArgs& a, lora_dtype_t in, int32_t head_dim, hipStream_t stream);
+
+struct PlanArgs {   // lora_kv_plan_t, and where its workspace's parts lie
+    const int32_t* new_rows;
+    const int32_t* adapter;
+    const int32_t* kv_len;
+    int32_t* kv_len_out;
+    int32_t* pages;
+    int64_t ldp;
+    int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* n_free_out;
+    const int32_t* group_off;
+    const int32_t* prefix_len;
+    int32_t* row_off;
+    int32_t* row_seq;
+    int32_t* row_adapter;
+    int32_t* row_pos;
+    int64_t* row_slot;
+    int32_t n_seqs, n_groups, page_shift, max_free, max_rows;
+    int32_t* status;
+    int32_t* take;   // [n_seqs + 1] granted pages before a sequence
+    int32_t* back;   // [n_seqs + 1] returned pages
+    int32_t* head;   // the stack's old height, and with the returned pages
+};
+size_t plan_bytes(int32_t n_seqs);
+hipError_t launch_kv_plan(PlanArgs a, void* ws, hipStream_t stream);
 
 // Attention over the pages.  A "problem" is a sequence over its own tokens
 // (kind 0) or a group of sequences over their shared prefix (kind 1).  Its
@@ -75,6 +118,7 @@ hipError_t launch_kv_append(const AppendArgs& a, lora_dtype_t in, lora_dtype_t c
 // waves and workgroups, more to the tiled kernel, which splits columns.
 constexpr int ATTN_FEW_COLS = 16;
 constexpr int ATTN_FEW_KEYS = 128;     // keys of a few-column work unit
+constexpr int ATTN_FEW_KEYS_Q8 = 256;  // in 8 bits
 constexpr int ATTN_FEW_WGS = 512;      // workgroups that share the units
 constexpr int ATTN_TILE_KEYS = 64;
 
@@ -115,6 +159,7 @@ struct AttnArgs {
     int32_t together;           // both forms in one launch
     int32_t decode;             // every sequence has few columns
     AttnPart part[2];
+    Q8Dev S;                    // a cache in 8 bits
 };
 struct AttnPlan {
     AttnArgs a;       // with part[] sized (pointers unset)
@@ -123,7 +168,8 @@ struct AttnPlan {
 };
 // max_rows, max_len: host bounds of a problem's rows and keys, per kind
 void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
-               const int32_t (&max_len)[2]);
+               const int32_t (&max_len)[2], bool in_8_bits = false);
 hipError_t launch_attn(const AttnArgs& a, lora_dtype_t dt, int32_t head_dim, hipStream_t stream);
+hipError_t launch_attn_q8(const AttnArgs& a, int32_t head_dim, hipStream_t stream);
 
 }  // namespace lora
