@@ -226,9 +226,9 @@ __device__ __forceinline__ void attn_few(const AttnArgs& a, int kind, int block,
         if (walk(Int<0>{})) walk(Int<1>{});
 
     };
-    few_pieces<ATTN_FEW_KEYS>(a, kind, block, blocks, sh, tid, lane, work,
+    few_pieces<ATTN_FEW_KEYS, 4>(a, kind, block, blocks, sh, tid, lane, work,
                               [&](const Prob& P, int h, bool whole, int slot) __attribute__((always_inline)) {
-                                  few_finish<T, D, WB>(a, kind, P, h, whole, slot, stage, wave, lane, m, l, acc);
+                                  few_finish<T, D, WB, 4>(a, kind, P, h, whole, slot, stage, wave, lane, m, l, acc);
                               });
 }
 
@@ -237,6 +237,7 @@ struct Plain {
     using T = T_;
     using TL = Tile<T, D_>;
     static constexpr int D = D_, FEW_KEYS = ATTN_FEW_KEYS, FEW_STAGE = FewStage<T, D>::WAVE;
+    static constexpr int FEW_WAVES = 4;
     static constexpr int WAVES = sizeof(T) * D <= 256 ? 2 : 1;
     static constexpr bool PAGED = PAGED_, Q8 = false;
     static __device__ __forceinline__ void few(const AttnArgs& a, int kind, int block, int blocks, uint8_t* stage, int* sh) {
@@ -245,7 +246,7 @@ struct Plain {
 };
 template <typename T, int D>
 struct PlainOf {
-    template <bool PAGED> using F = Plain<T, D, PAGED>;
+    template <bool PAGED, bool> using F = Plain<T, D, PAGED>;
 };
 template <typename T, int D>
 hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
@@ -256,7 +257,6 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 
 void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t (&n_prob)[2], const int32_t (&max_rows)[2],
                const int32_t (&max_len)[2], bool in_8_bits) {
-    const int few_keys = in_8_bits ? ATTN_FEW_KEYS_Q8 : ATTN_FEW_KEYS;
     // The workspace's parts grow with every bound and do not rest on the
     // window (with one there are fewer keys, so fewer shared units and no more
     // splits), so that one allocation serves every smaller batch.
@@ -280,6 +280,13 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
     const int64_t wide_items = ((int64_t)a.B.n_rows * a.share / 256 + std::min(n_prob[0], a.B.n_rows)) * hkv;
     a.tile_cols = (a.join && a.decode) || head_dim * elem_bytes > 256 || wide_items < 256 ||
                           std::max(cols[0], n_prob[1] > 0 ? cols[1] : 0) <= 128 ? 128 : 256;
+    // Both forms in one launch where both have work and tiles of 128 columns
+    // do: 32 requests behind a prefix of 4096 tokens 31 us, in two launches
+    // 43; a few fp32 rows and a short prompt 21 us, in two launches 30.
+    const bool tiles = (n_prob[0] > 0 && cols[0] > ATTN_FEW_COLS) || (n_prob[1] > 0 && cols[1] > ATTN_FEW_COLS);
+    a.together = a.tile_cols == 128 && tiles && (n_prob[0] > 0 || n_prob[1] > 0) && a.share <= ATTN_FEW_COLS && a.B.n_rows > 0;
+    const int few_waves = in_8_bits ? few_waves_q8(head_dim, a.together) : 4;
+    const int few_keys = in_8_bits ? few_waves * ATTN_WAVE_KEYS_Q8 : ATTN_FEW_KEYS;
     for (int k = 0; k < 2; ++k) {
         AttnPart& W = a.part[k];
         W = AttnPart{};
@@ -315,9 +322,11 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
                 return u <= 4 || (u <= 16 && pairs >= 8 * u) || pairs >= 4096;
             };
             W.few = direct(units, heads) ? 1 : 2;
-            W.few_grid = W.few == 1 ? n_prob[k] * hkv : ATTN_FEW_WGS;
+            W.few_grid = W.few == 1 ? n_prob[k] * hkv : ATTN_FEW_WGS * 4 / few_waves;
             if (W.few == 2) a.need_join = 1;
-            if (!direct(ceil_div(max_len[k], few_keys), hkv)) {   // of a single sequence or group
+            // (a smaller batch may have both forms in one launch, with smaller units)
+            const int least = in_8_bits ? few_waves_q8(head_dim, true) * ATTN_WAVE_KEYS_Q8 : few_keys;
+            if (!direct(ceil_div(max_len[k], least), hkv)) {   // of a single sequence or group
                 P.off[k][0] = take((size_t)n_prob[k] * hkv * sizeof(int2));
                 P.off[k][1] = take((size_t)2 * ATTN_FEW_WGS * 16 * head_dim * 4);
                 P.off[k][2] = take((size_t)2 * ATTN_FEW_WGS * 16 * sizeof(float2));
@@ -363,11 +372,6 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
             }
         }
     }
-    // Both forms in one launch where both have work and tiles of 128 columns
-    // do: 32 requests behind a prefix of 4096 tokens 31 us, in two launches
-    // 43; a few fp32 rows and a short prompt 21 us, in two launches 30.
-    a.together = a.tile_cols == 128 && a.part[0].tile_grid + a.part[1].tile_grid > 0 &&
-                 a.part[0].few_grid + a.part[1].few_grid > 0;
     if (a.join) {
         for (int k = 0; k < 2; ++k) {
             P.off[k][6] = take((size_t)a.B.n_rows * a.n_q_heads * ((size_t)head_dim * 4 + sizeof(float2)));

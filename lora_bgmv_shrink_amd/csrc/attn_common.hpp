@@ -628,40 +628,46 @@ __device__ __forceinline__ int64_t scale_at(const AttnArgs& a, int page, int key
     return (int64_t)page * a.S.page_stride + (int64_t)(block * (int)a.S.block_stride) + (int64_t)h * a.S.head_stride;
 }
 
-// A workgroup's request of a tile of 64 keys in 8 bits: NT pieces of 16
-// numbers a thread, keys' and then values', in registers until they are
-// widened into the staged tile of bf16.  (Widened when they are staged, a
-// number is widened once for all waves.)
-template <int D, int NW>
+// A workgroup's request of a tile of 64 keys in 8 bits: NT pieces of 16 numbers
+// a thread, keys' and then values', in registers until they are widened into
+// the staged tile of bf16 (so a number is widened once for all waves).
+template <int D, bool PAGED, int NW>
 struct TileRequestQ8 {
     using TL = Tile<bf16, D>;
     static constexpr int LPR = D / 16;                                 // pieces of a key
     static constexpr int RPL = 64 / LPR;                               // keys of a wave's load
     static constexpr int NT = 2 * ATTN_TILE_KEYS * LPR / (64 * NW);    // loads, LPR waves' for each tensor
     u32x4_t r[NT];
-    float ks, vs;   // scales of key `lane`
-    __device__ __forceinline__ TileRequestQ8(const AttnArgs&, int, int) {}
-    __device__ __forceinline__ void load(const AttnArgs& a, int64_t place, int64_t scales, int wave, int lane) {
-        ks = a.S.k_scale[scales];
-        vs = a.S.v_scale[scales];
+    float s[NT];    // scales
+    int at[NT];     // places in the staged tile
+    __device__ __forceinline__ TileRequestQ8(int wave, int lane) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int L = n * NW + wave;
-            const int64_t off = __shfl(place, (L % LPR) * RPL + lane / LPR, 64) + (lane % LPR) * 16;
-            r[n] = *(const u32x4_t*)((const uint8_t*)(L < LPR ? a.C.k : a.C.v) + off);
+            const int L = n * NW + wave, row = (L % LPR) * RPL + lane / LPR, piece = 2 * (lane % LPR);
+            at[n] = L < LPR ? TL::k_at(row, piece) : ATTN_TILE_KEYS * TL::RB + TL::v_at(row, piece);
         }
     }
-    // into a staged tile: keys at `to`, values TB bytes further
-    __device__ __forceinline__ void stash(uint8_t* to, int wave, int lane) const {
+    // place, scales: where key `lane` of the tile and its scales lie
+    __device__ __forceinline__ void load(const AttnArgs& a, int64_t place, int64_t scales, int wave, int lane) {
+        const int row = lane / LPR;
+        // keys of a load start at a multiple of RPL: their blocks follow from the first one's
+        const int block = PAGED ? (row >> a.S.block_shift) * (int)a.S.block_stride : 0;
+        const uint32_t in = (uint32_t)((PAGED ? row * (int)a.C.token_stride : 0) + (lane % LPR) * 16);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int L = n * NW + wave;
-            const bool v = L >= LPR;
-            const int row = (L % LPR) * RPL + lane / LPR, piece = 2 * (lane % LPR);
-            const float s = power_of(__shfl(v ? vs : ks, row, 64));
-            uint8_t* at = to + (v ? ATTN_TILE_KEYS * TL::RB + TL::v_at(row, piece) : TL::k_at(row, piece));
-            *(bf16x8_t*)at = widen(r[n].x, r[n].y, s);
-            *(bf16x8_t*)(to + ((at - to) ^ 16)) = widen(r[n].z, r[n].w, s);
+            const int L = n * NW + wave, row0 = (L % LPR) * RPL;
+            const int64_t off = PAGED ? lane_of(place, row0) : __shfl(place, row0 + row, 64);
+            const int64_t sc = PAGED ? lane_of(scales, row0) : __shfl(scales, row0 + row, 64);
+            s[n] = ((L < LPR ? a.S.k_scale : a.S.v_scale) + sc)[block];
+            r[n] = *(const u32x4_t*)((const uint8_t*)(L < LPR ? a.C.k : a.C.v) + off + in);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* to) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float by = power_of(s[n]);
+            *(bf16x8_t*)(to + at[n]) = widen(r[n].x, r[n].y, by);
+            *(bf16x8_t*)(to + (at[n] ^ 16)) = widen(r[n].z, r[n].w, by);
         }
     }
 };
@@ -689,7 +695,7 @@ __device__ __forceinline__ uint64_t sees(const AttnArgs& a, int col_pos, int lo,
 // lengths; a run's first and last (problem, head) may be partial and go to
 // slots that the join adds.  Otherwise a workgroup takes one (problem, head)
 // whole.
-template <int FK, class WORK, class FINISH>
+template <int FK, int NW, class WORK, class FINISH>
 __device__ __forceinline__ void few_pieces(const AttnArgs& a, int kind, int block, int blocks, int* sh, int tid, int lane,
                                            WORK work, FINISH finish) {
     const int hkv = a.C.n_kv_heads;
@@ -722,7 +728,7 @@ __device__ __forceinline__ void few_pieces(const AttnArgs& a, int kind, int bloc
             return u;
         };
         int base = 0;
-        if (!locate<4>(n_prob, units, pick, tid, sh, p, base)) return;
+        if (!locate<NW>(n_prob, units, pick, tid, sh, p, base)) return;
         P = load_prob<true>(a, kind, p, lane);
         R = range_of(P);
         h = (u - base) / R.n;
@@ -765,10 +771,10 @@ __device__ __forceinline__ void few_pieces(const AttnArgs& a, int kind, int bloc
     }
 }
 
-// Joins the four waves' results of a piece and writes them: to their place, or
+// Joins the NW waves' results of a piece and writes them: to their place, or
 // as partial results.  WB: LDS bytes of a wave's stage.  m, l and acc are a
 // lane's largest score, sum of its weights and elements of O.
-template <typename T, int D, int WB>
+template <typename T, int D, int WB, int NW>
 __device__ __forceinline__ void few_finish(const AttnArgs& a, int kind, const Prob& P, int h, bool whole, int slot,
                                            uint8_t* stage, int wave, int lane, float m, float l,
                                            const f32x4_t (&acc)[D / 16]) {
@@ -790,20 +796,20 @@ __device__ __forceinline__ void few_finish(const AttnArgs& a, int kind, const Pr
     for (int t = 0; t < D / 16; ++t)
         *(float4*)(so + l16 * OP + t * 16 + g4 * 4) = float4{acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
     __syncthreads();
-    {
+    if (NW == 4 || tid < 256) {
         constexpr int N = D / 16;   // elements per thread, of column tid / 16
         constexpr int WF = WB / 4;  // floats of a wave's stage
         const int col = tid >> 4, d = (tid & 15) * N;
         const float* all = (const float*)stage;
-        float mw[4], M = -kInf, sum = 0.f, v[N];
+        float mw[NW], M = -kInf, sum = 0.f, v[N];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < NW; ++w) {
             mw[w] = all[w * WF + 16 * OP + col];
             M = fmaxf(M, mw[w]);
         }
         const float ref = M == -kInf ? 0.f : M;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < NW; ++w) {
             mw[w] = exp2_fast((mw[w] - ref) * c);
             sum += mw[w] * all[w * WF + 16 * OP + 16 + col];
         }
@@ -811,7 +817,7 @@ __device__ __forceinline__ void few_finish(const AttnArgs& a, int kind, const Pr
         for (int e = 0; e < N; e += 4) {
             float4 x{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const float4 y = *(const float4*)(all + w * WF + col * OP + d + e);
                 x.x += mw[w] * y.x;
                 x.y += mw[w] * y.y;
@@ -997,7 +1003,10 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
         if constexpr (FORM::Q8) scales = scale_at(a, page_ok ? id : 0, X.key + lane, h);
         return (uint64_t)__ballot(seen && page_ok);
     };
-    std::conditional_t<FORM::Q8, TileRequestQ8<D, NW>, TileRequest<T, D, PAGED, NW>> request(a, wave, lane);
+    auto request = [&]() __attribute__((always_inline)) {
+        if constexpr (FORM::Q8) return TileRequestQ8<D, PAGED, NW>(wave, lane);
+        else return TileRequest<T, D, PAGED, NW>(a, wave, lane);
+    }();
     const uint32_t stage_at = lds_offset(stage);
     // the loads from..to - 1 of a tile into a buffer; in 8 bits all of them
     // with the first, into registers
@@ -1012,7 +1021,7 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
     };
     // what was loaded in 8 bits goes into its buffer, which nobody reads any more
     auto stash = [&](int buf) __attribute__((always_inline)) {
-        if constexpr (FORM::Q8) request.stash(stage + buf * 2 * TB, wave, lane);
+        if constexpr (FORM::Q8) request.store(stage + buf * 2 * TB);
     };
     constexpr int Q1 = (NL + 3) / 4, Q2 = (NL + 1) / 2, Q3 = (3 * NL + 3) / 4;   // a quarter each
 
@@ -1240,10 +1249,10 @@ __device__ __forceinline__ void attn_tile(const AttnArgs& a, int kind, int block
 // One launch of a form over own tokens and shared prefixes: a workgroup's
 // number says which.
 template <class FORM>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(FORM::WAVES)))
+__global__ __launch_bounds__(64 * FORM::FEW_WAVES) __attribute__((amdgpu_waves_per_eu(FORM::WAVES)))
 void k_attn_few(AttnArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t stage[4 * FORM::FEW_STAGE];
-    __shared__ int sh[8];
+    __shared__ __attribute__((aligned(16))) uint8_t stage[FORM::FEW_WAVES * FORM::FEW_STAGE];
+    __shared__ int sh[FORM::FEW_WAVES + 4];
     const int n0 = a.part[0].few_grid, b = blockIdx.x;
     const int kind = b < n0 ? 0 : 1;
     FORM::few(a, kind, kind ? b - n0 : b, a.part[kind].few_grid, stage, sh);
@@ -1456,42 +1465,42 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int by_row, int r
     if (a.lse && sl == 0) a.lse[rh] = lse_of(a, M, L);
 }
 
-// FORM<false> and FORM<true>: the form for pages that hold less than a load's keys
-// and for others.
-template <template <bool> class FORM>
+// FORM<PAGED, TOGETHER>: the form for pages that hold a load's keys, or less;
+// for both forms in one launch, or in two.
+template <template <bool, bool> class FORM>
 hipError_t launch_form(const AttnArgs& a, bool paged, hipStream_t stream) {
-    using T = typename FORM<true>::T;
-    constexpr int D = FORM<true>::D;
+    using T = typename FORM<true, false>::T;
+    constexpr int D = FORM<true, false>::D;
     const unsigned tiles = a.part[0].tile_grid + a.part[1].tile_grid, few = a.part[0].few_grid + a.part[1].few_grid;
     if (a.together) {
-        if (paged) hipLaunchKernelGGL((k_attn_both<FORM<true>>), dim3(tiles + few), dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((k_attn_both<FORM<false>>), dim3(tiles + few), dim3(256), 0, stream, a);
+        if (paged) hipLaunchKernelGGL((k_attn_both<FORM<true, true>>), dim3(tiles + few), dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((k_attn_both<FORM<false, true>>), dim3(tiles + few), dim3(256), 0, stream, a);
     }
-    // in 8 bits a tile's loads do not depend on the page size
-    using SMALL = std::conditional_t<FORM<true>::Q8, FORM<true>, FORM<false>>;
     if (tiles && !a.together) {
         const dim3 grid(tiles), block(2 * a.tile_cols);
         bool wide = false;
         if constexpr (kWide<T, D>) {
             wide = a.tile_cols == 256;
-            if (wide && paged) hipLaunchKernelGGL((k_attn_tile<FORM<true>, 8>), grid, block, 0, stream, a);
-            else if (wide) hipLaunchKernelGGL((k_attn_tile<SMALL, 8>), grid, block, 0, stream, a);
+            if (wide && paged) hipLaunchKernelGGL((k_attn_tile<FORM<true, false>, 8>), grid, block, 0, stream, a);
+            else if (wide) hipLaunchKernelGGL((k_attn_tile<FORM<false, false>, 8>), grid, block, 0, stream, a);
         }
         if (!wide) {
-            if (paged) hipLaunchKernelGGL((k_attn_tile<FORM<true>, 4>), grid, block, 0, stream, a);
-            else hipLaunchKernelGGL((k_attn_tile<SMALL, 4>), grid, block, 0, stream, a);
+            if (paged) hipLaunchKernelGGL((k_attn_tile<FORM<true, false>, 4>), grid, block, 0, stream, a);
+            else hipLaunchKernelGGL((k_attn_tile<FORM<false, false>, 4>), grid, block, 0, stream, a);
         }
     }
     if (few && !a.together) {
-        if (paged) hipLaunchKernelGGL((k_attn_few<FORM<true>>), dim3(few), dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((k_attn_few<FORM<false>>), dim3(few), dim3(256), 0, stream, a);
+        if (paged) hipLaunchKernelGGL((k_attn_few<FORM<true, false>>), dim3(few), dim3(64 * FORM<true, false>::FEW_WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((k_attn_few<FORM<false, false>>), dim3(few), dim3(64 * FORM<true, false>::FEW_WAVES), 0, stream, a);
     }
     if (a.need_join) {
         const int by_row = a.part[0].slots;
         const int few_rows = std::max(1, std::min(ATTN_FEW_COLS / a.share, a.part[0].max_rows));
         const int64_t rows = by_row ? a.B.n_rows : (int64_t)a.B.n_seqs * few_rows;
-        hipLaunchKernelGGL((k_attn_join<D, FORM<true>::FEW_KEYS>), dim3((unsigned)ceil_div(rows * ceil_div(a.n_q_heads, 4), 4)), dim3(256), 0,
-                           stream, a, by_row, few_rows);
+        const dim3 grid((unsigned)ceil_div(rows * ceil_div(a.n_q_heads, 4), 4));
+        constexpr int ALONE = FORM<true, false>::FEW_KEYS, BESIDE = FORM<true, true>::FEW_KEYS;
+        if (a.together) hipLaunchKernelGGL((k_attn_join<D, BESIDE>), grid, dim3(256), 0, stream, a, by_row, few_rows);
+        else hipLaunchKernelGGL((k_attn_join<D, ALONE>), grid, dim3(256), 0, stream, a, by_row, few_rows);
     }
     return hipGetLastError();
 }

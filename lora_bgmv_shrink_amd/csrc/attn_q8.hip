@@ -39,11 +39,12 @@ __device__ __forceinline__ bool has_nan(const u32x4_t& v) {   // e4m3: seven bit
 // the transposed reading, and are widened behind it; there a lane holds eight
 // keys of one dimension, so their scales go into the weights, which are a
 // power of two times what they were and lose nothing by it.
-template <int D, bool PAGED>
+template <int D, bool PAGED, int NW>
 __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int block, int blocks, uint8_t* stage, int* sh) {
     using BT = Bytes<D>;
     using O = Op<bf16>;
-    constexpr int KW = ATTN_FEW_KEYS_Q8 / 4;    // keys of a wave's unit
+    constexpr int KW = ATTN_WAVE_KEYS_Q8;       // keys of a wave's unit
+    constexpr int KEYS = NW * KW;
     constexpr int G = KW / 16;                  // groups of 16
     constexpr int KC = D / 64;                  // pieces of a lane's key
     constexpr int NV = BT::LPR;                 // pieces of values per lane
@@ -76,7 +77,7 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
 #pragma unroll
             for (int s = 0; s < KC; ++s)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) qf[s][e] = there ? O::load(q + s * 64 + g4 * 16 + e * 8) : O::zero();
+                for (int e = 0; e < 2; ++e) qf[s][e] = there ? O::load(q + g4 * (D / 4) + s * 16 + e * 8) : O::zero();
             int seq_rows;
             if (there) col_pos = kind == 0 ? P.pos0 + j : a.window > 0 ? row_position(a, P.r0 + j, seq_rows) : P.pos1;
         }
@@ -88,7 +89,19 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
             for (int x = 1; x < 16; x <<= 1) lo_pos = min(lo_pos, __shfl_xor(lo_pos, x, 64));
             lo_pos = __builtin_amdgcn_readfirstlane(lo_pos);
         }
-        auto base_of = [&](int x) __attribute__((always_inline)) { return R.tile(x) * ATTN_FEW_KEYS_Q8 + wave * KW; };
+        auto base_of = [&](int x) __attribute__((always_inline)) { return R.tile(x) * KEYS + wave * KW; };
+        // A wave leaves out units at the range's ends of whose keys its rows see
+        // none (with a wave of 64 keys, most of a short sequence's).
+        auto unseen = [&](int x) __attribute__((always_inline)) {
+            const int key = base_of(x), at = P.key0 + key;
+            return key >= P.len || at > P.pos1 ||
+                   (a.window > 0 && at + KW - 1 <= lo_pos - a.window && at >= a.n_sink);
+        };
+        while (n > 0 && unseen(i + n - 1)) --n;
+        while (n > 0 && unseen(i)) {
+            ++i;
+            --n;
+        }
         // page number of key `lane` of the wave's unit x, -1: none
         auto load_id = [&](int x) __attribute__((always_inline)) {
             const int key = base_of(x) + lane;
@@ -107,15 +120,19 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
             scale = scale_at(a, page_ok ? id : 0, key, h);
             return (uint64_t)__ballot(seen && page_ok);
         };
+        // Keys through the caches, since two loads share a line (past them the
+        // second fetches it again: 32 requests of up to 2047 tokens 25 us, so
+        // 21.5); values, whole lines, past them (8 requests of 16 k to 60 k tokens
+        // 99 us, both tensors through the caches 107).
         u32x4_t rk[G][KC], rv[NV];
         float ks, vs;   // scales of key `lane`
         auto request_k = [&](int64_t place) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const int64_t off = PAGED ? lane_of(place, 16 * j) : __shfl(place, 16 * j + l16, 64);
-                const uint32_t in = (uint32_t)((PAGED ? l16 * (int)a.C.token_stride : 0) + g4 * 16);
+                const uint32_t in = (uint32_t)((PAGED ? l16 * (int)a.C.token_stride : 0) + g4 * (D / 4));
 #pragma unroll
-                for (int s = 0; s < KC; ++s) rk[j][s] = piece_at((const uint8_t*)a.C.k + off + in + s * 64);
+                for (int s = 0; s < KC; ++s) rk[j][s] = *(const u32x4_t*)((const uint8_t*)a.C.k + off + in + s * 16);
             }
         };
         auto request_v = [&](int64_t place) __attribute__((always_inline)) {
@@ -140,14 +157,21 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
             for (int t = 0; t < D / 16; ++t) acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             bool odd = false;
             if (n == 0) return false;
-            int id = load_id(i);
+            // Loads return in order, and a wait is for a number of loads that may
+            // still be out: page numbers and scales are requested before the
+            // pieces that stay in flight when they are waited for, here as in
+            // the loop.
+            const int id0 = load_id(i);
+            int id = load_id(min(i + 1, i + n - 1));
             int64_t place, scale;
-            uint64_t bits = seen_of(i, id, place, scale);
+            uint64_t bits = seen_of(i, id0, place, scale);
             ks = a.S.k_scale[scale];
             vs = a.S.v_scale[scale];
+            __builtin_amdgcn_sched_barrier(0);
             request_k(place);
+            __builtin_amdgcn_sched_barrier(0);
             request_v(place);
-            id = load_id(min(i + 1, i + n - 1));
+            __builtin_amdgcn_sched_barrier(0);
             for (int x = i; x < i + n; ++x) {
                 const int next = min(x + 1, i + n - 1);   // after the last unit that one again: nothing branches
                 const int lo = P.key0 + base_of(x);
@@ -159,21 +183,27 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 // element r of s[j]: key 16 j + 4 g4 + r, this lane's column
                 f32x4_t s[G];
+                float by[G];
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    const float by = scales_at[16 * j + l16];
+                    by[j] = scales_at[16 * j + l16];
                     s[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                }
+                // (the groups' sums in turn: a product waits for the one before it)
 #pragma unroll
-                    for (int t = 0; t < KC; ++t) {
-                        s[j] = O::mma16(widen(rk[j][t].x, rk[j][t].y, by), qf[t][0], s[j]);
-                        s[j] = O::mma16(widen(rk[j][t].z, rk[j][t].w, by), qf[t][1], s[j]);
-                    }
+                for (int t = 0; t < KC; ++t) {
+#pragma unroll
+                    for (int j = 0; j < G; ++j) s[j] = O::mma16(widen(rk[j][t].x, rk[j][t].y, by[j]), qf[t][0], s[j]);
+#pragma unroll
+                    for (int j = 0; j < G; ++j) s[j] = O::mma16(widen(rk[j][t].z, rk[j][t].w, by[j]), qf[t][1], s[j]);
                 }
                 bits = seen_of(next, id, place, scale);
                 id = load_id(min(x + 2, i + n - 1));
                 ks = a.S.k_scale[scale];
                 vs = a.S.v_scale[scale];
+                __builtin_amdgcn_sched_barrier(0);
                 request_k(place);
+                __builtin_amdgcn_sched_barrier(0);
                 if (!all_see) {
                     asm volatile("");
                     hide_rows<NV>(rv, bits_x, here(lane) / BT::LPR, RPL);
@@ -230,17 +260,32 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
                 }
                 const int va = here(vop);
                 const bool clean = ODD && !all_see;
+                // values of dimensions 16 t .. and keys 32 u ..: read AHEAD products before they are multiplied
+                constexpr int AHEAD = 8, NP = G / 2 * (D / 16);
+                typedef int i32x2_t __attribute__((ext_vector_type(2)));
+                i32x2_t b[AHEAD];
+                auto read = [&](int p) __attribute__((always_inline)) {
+                    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t*)(
+                        mine_at + 32 * (p / (D / 16)) * D + (va ^ ((p % (D / 16)) << 4))));
+                };
 #pragma unroll
-                for (int u = 0; u < G / 2; ++u)
+                for (int p = 0; p < AHEAD; ++p) b[p] = read(p);
 #pragma unroll
-                    for (int t = 0; t < D / 16; ++t) {
-                        typedef int i32x2_t __attribute__((ext_vector_type(2)));
-                        const i32x2_t b = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                            (__attribute__((address_space(3))) i32x2_t*)(mine_at + 32 * u * D + (va ^ (t << 4))));
-                        bf16x8_t vf = widen((uint32_t)b.x, (uint32_t)b.y, 1.f);
-                        if (clean) O::clean(vf);
-                        acc[t] = O::mma16(vf, pf[u], acc[t]);
+                for (int p = 0; p < NP; ++p) {
+                    bf16x8_t vf = widen((uint32_t)b[p % AHEAD].x, (uint32_t)b[p % AHEAD].y, 1.f);
+                    if (p + AHEAD < NP) b[p % AHEAD] = read(p + AHEAD);
+                    if (clean) O::clean(vf);
+                    acc[p % (D / 16)] = O::mma16(vf, pf[p / (D / 16)], acc[p % (D / 16)]);
+                }
+                if constexpr (!ODD) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                        if (p + AHEAD < NP) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                     }
+                }
                 if (clean) {
                     const uint64_t seen = sees(a, col_pos, lo, bits_x);
                     for (int k = 0; k < KW; ++k) {
@@ -266,26 +311,27 @@ __device__ __forceinline__ void attn_few_q8(const AttnArgs& a, int kind, int blo
         };
         if (walk(Int<0>{})) walk(Int<1>{});
     };
-    few_pieces<ATTN_FEW_KEYS_Q8>(a, kind, block, blocks, sh, tid, lane, work,
+    few_pieces<KEYS, NW>(a, kind, block, blocks, sh, tid, lane, work,
                                  [&](const Prob& P, int h, bool whole, int slot) __attribute__((always_inline)) {
-                                     few_finish<bf16, D, WB>(a, kind, P, h, whole, slot, stage, wave, lane, m, l, acc);
+                                     few_finish<bf16, D, WB, NW>(a, kind, P, h, whole, slot, stage, wave, lane, m, l, acc);
                                  });
 }
 
-template <int D_, bool PAGED_>
+template <int D_, bool PAGED_, bool TOGETHER>
 struct InBytes {
     using T = bf16;
     using TL = Tile<T, D_>;
-    static constexpr int D = D_, FEW_KEYS = ATTN_FEW_KEYS_Q8, FEW_STAGE = FewStageQ8<D>::WAVE;
+    static constexpr int D = D_, FEW_WAVES = few_waves_q8(D, TOGETHER), FEW_KEYS = FEW_WAVES * ATTN_WAVE_KEYS_Q8;
+    static constexpr int FEW_STAGE = FewStageQ8<D>::WAVE;
     static constexpr int WAVES = D <= 128 ? 2 : 1;
     static constexpr bool PAGED = PAGED_, Q8 = true;
     static __device__ __forceinline__ void few(const AttnArgs& a, int kind, int block, int blocks, uint8_t* stage, int* sh) {
-        attn_few_q8<D, PAGED>(a, kind, block, blocks, stage, sh);
+        attn_few_q8<D, PAGED, FEW_WAVES>(a, kind, block, blocks, stage, sh);
     }
 };
 template <int D>
 struct InBytesOf {
-    template <bool PAGED> using F = InBytes<D, PAGED>;
+    template <bool PAGED, bool TOGETHER> using F = InBytes<D, PAGED, TOGETHER>;
 };
 
 }  // namespace

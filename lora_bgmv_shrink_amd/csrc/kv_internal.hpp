@@ -118,9 +118,14 @@ hipError_t launch_kv_plan(PlanArgs a, void* ws, hipStream_t stream);
 // waves and workgroups, more to the tiled kernel, which splits columns.
 constexpr int ATTN_FEW_COLS = 16;
 constexpr int ATTN_FEW_KEYS = 128;     // keys of a few-column work unit
-constexpr int ATTN_FEW_KEYS_Q8 = 256;  // in 8 bits
+constexpr int ATTN_WAVE_KEYS_Q8 = 64;  // in 8 bits: of a wave
 constexpr int ATTN_FEW_WGS = 512;      // workgroups that share the units
 constexpr int ATTN_TILE_KEYS = 64;
+
+// Waves of a few-column workgroup in 8 bits.  Beside tiles it has their four;
+// alone eight, so that a (problem, key head) that has a workgroup to itself has
+// a whole CU's waves.  Heads of 256 need the registers of two waves.
+constexpr int few_waves_q8(int head_dim, bool together) { return together || head_dim > 128 ? 4 : 8; }
 
 struct AttnPart {       // one kind's kernels and where their partial results lie
     int32_t max_rows;   // host bounds that the sizes below rest on: a problem's rows
