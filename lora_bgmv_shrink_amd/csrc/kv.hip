@@ -18,7 +18,7 @@ namespace {
 
 template <typename TI, typename TO, int D>
 __global__ __launch_bounds__(KA_WAVES * 64) void k_kv_append(AppendArgs a, int it) {
-    append_row<TI, TO, D>(a, it, blockIdx.x, blockIdx.y);
+    append_row<TI, TO, D, false>(a, it, blockIdx.x, blockIdx.y);
 }
 
 template <typename TI, typename TO>

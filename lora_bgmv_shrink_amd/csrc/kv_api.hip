@@ -252,7 +252,7 @@ lora_status_t check_plan(const lora_kv_plan_t* p, PlanArgs& a) {
     a = PlanArgs{p->new_rows, p->adapter, p->kv_len, p->kv_len_out, p->pages, p->ldp, p->free_pages, p->n_free,
                  p->n_free_out, p->group_off, p->prefix_len, p->row_off, p->row_seq, p->row_adapter, p->row_pos,
                  p->row_slot, p->n_seqs, p->n_groups, __builtin_ctz((unsigned)p->page_size), p->max_free, p->max_rows,
-                 nullptr, nullptr, nullptr, nullptr};
+                 nullptr, nullptr, nullptr, nullptr, nullptr};
     return LORA_OK;
 }
 

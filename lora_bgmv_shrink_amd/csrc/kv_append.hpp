@@ -48,7 +48,9 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 // piece that holds its partners; otherwise two neighbouring pieces.  64 is a
 // multiple of a head's items, so a lane keeps the same place in every head it
 // visits and loads its cosines and sines once.
-template <typename TI, typename TO, int D>
+// EARLY: the row's elements are requested before its place is looked up, and
+// the lookup takes fewer steps.
+template <typename TI, typename TO, int D, bool EARLY>
 __device__ __forceinline__ void append_row(const AppendArgs& a, int it, int block_row, int run) {
     constexpr int IPH = D / 16;   // items per head
     const int lane = threadIdx.x & 63;
@@ -74,14 +76,43 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int it, int bloc
         e1 = e0 + 8;
     }
 
+    const int end = min(n_items, (int)(run + 1) * it * 64), begin = run * it * 64 + lane;
+    Eight<TI> x0[KA_BATCH], x1[KA_BATCH];
+    auto request = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < KA_BATCH; ++u) {
+            const int i = i0 + u * 64;
+            if (i >= end) break;
+            const int h = i / IPH;
+            const TI* src;
+            if (h < a.n_q_heads) src = (const TI*)a.q + (int64_t)row * a.ldq + h * D;
+            else if (h < a.n_q_heads + a.C.n_kv_heads)
+                src = (const TI*)a.k + (int64_t)row * a.ldk + (h - a.n_q_heads) * D;
+            else src = (const TI*)a.v + (int64_t)row * a.ldv + (h - a.n_q_heads - a.C.n_kv_heads) * D;
+            const bool plain = h >= a.n_q_heads + a.C.n_kv_heads && halves;
+            x0[u].load(src + (plain ? c * 16 : e0));
+            x1[u].load(src + (plain ? c * 16 + 8 : e1));
+        }
+    };
+    if (EARLY && begin < end) request(begin);
+
     // the row's place: sequence, index among its own tokens, page
-    const int s = wave_find_run(B.row_off, B.n_seqs, row, lane);
-    bool ok = s < B.n_seqs;
+    int s, r0 = 0, r1 = 0, len = 0;
+    bool ok;
+    if constexpr (EARLY) {
+        ok = wave_find_seq(B, row, lane, [](int, int off) { return off; }, s, r0, r1, len);
+    } else {
+        s = wave_find_run(B.row_off, B.n_seqs, row, lane);
+        ok = s < B.n_seqs;
+    }
     int pos = 0;
     int64_t slot = 0;
     if (ok) {
-        const int r1 = B.row_off[s + 1];
-        const int t = B.kv_len[s] - (r1 - row);
+        if constexpr (!EARLY) {
+            r1 = B.row_off[s + 1];
+            len = B.kv_len[s];
+        }
+        const int t = len - (r1 - row);
         int before = 0;
         if (B.n_groups) {
             const int g = wave_find_run(B.group_off, B.n_groups, s, lane);
@@ -112,23 +143,8 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, int it, int bloc
         }
     }
 
-    const int end = min(n_items, (int)(run + 1) * it * 64);
-    for (int i0 = run * it * 64 + lane; i0 < end; i0 += KA_BATCH * 64) {
-        Eight<TI> x0[KA_BATCH], x1[KA_BATCH];
-#pragma unroll
-        for (int u = 0; u < KA_BATCH; ++u) {
-            const int i = i0 + u * 64;
-            if (i >= end) break;
-            const int h = i / IPH;
-            const TI* src;
-            if (h < a.n_q_heads) src = (const TI*)a.q + (int64_t)row * a.ldq + h * D;
-            else if (h < a.n_q_heads + a.C.n_kv_heads)
-                src = (const TI*)a.k + (int64_t)row * a.ldk + (h - a.n_q_heads) * D;
-            else src = (const TI*)a.v + (int64_t)row * a.ldv + (h - a.n_q_heads - a.C.n_kv_heads) * D;
-            const bool plain = h >= a.n_q_heads + a.C.n_kv_heads && halves;
-            x0[u].load(src + (plain ? c * 16 : e0));
-            x1[u].load(src + (plain ? c * 16 + 8 : e1));
-        }
+    for (int i0 = begin; i0 < end; i0 += KA_BATCH * 64) {
+        if (!EARLY || i0 != begin) request(i0);
 #pragma unroll
         for (int u = 0; u < KA_BATCH; ++u) {
             const int i = i0 + u * 64;

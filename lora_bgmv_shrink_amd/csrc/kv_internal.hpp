@@ -48,6 +48,31 @@ __device__ inline int wave_find_run(const int32_t* __restrict__ off, int n, int 
     return lo;
 }
 
+// The same search for a row's sequence s, or for what grows with it (at(i, off[i])
+// ascending; s the last with at <= key), with its first row, the next one's and
+// its length, which come with the last probes.  false: past the last sequence.
+template <class AT>
+__device__ inline bool wave_find_seq(const KvBatchDev& B, int key, int lane, AT at, int& s, int& r0, int& r1, int& len) {
+    int lo = 0, hi = B.n_seqs;
+    while (hi - lo > 63) {
+        const int step = (hi - lo + 63) >> 6;
+        const int i = lo + (lane + 1) * step;
+        const bool le = i <= hi && at(i, B.row_off[i]) <= key;
+        const int c = __popcll(__ballot(le));
+        hi = min(hi, lo + (c + 1) * step - 1);
+        lo += c * step;
+    }
+    const int i = min(lo + lane, B.n_seqs);
+    const int off = B.row_off[i], n = i < B.n_seqs ? B.kv_len[i] : 0;
+    const int c = __popcll(__ballot(lane > 0 && lo + lane <= hi && at(i, off) <= key));
+    s = lo + c;
+    if (s >= B.n_seqs) return false;
+    r0 = __builtin_amdgcn_readlane(off, c);
+    len = __builtin_amdgcn_readlane(n, c);
+    r1 = c < 63 ? __builtin_amdgcn_readlane(off, c + 1) : B.row_off[s + 1];
+    return true;
+}
+
 // What a cache in 8 bits has besides (KvDev's strides are then bytes).
 constexpr int Q8_LEAST = -100, Q8_MOST = 100;   // exponents of a scale
 struct Q8Dev {
@@ -106,7 +131,8 @@ struct PlanArgs {   // lora_kv_plan_t, and where its workspace's parts lie
     int32_t* status;
     int32_t* take;   // [n_seqs + 1] granted pages before a sequence
     int32_t* back;   // [n_seqs + 1] returned pages
-    int32_t* head;   // the stack's old height, and with the returned pages
+    int32_t* len;    // [n_seqs] tokens before the step
+    int32_t* head;   // the stack's old height, and with the returned pages; granted rows and pages
 };
 size_t plan_bytes(int32_t n_seqs);
 hipError_t launch_kv_plan(PlanArgs a, void* ws, hipStream_t stream);

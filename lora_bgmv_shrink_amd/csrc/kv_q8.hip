@@ -13,6 +13,12 @@
 // matrix cores' widening takes.
 //
 // Queries go the way of the other caches, rounded to bf16.
+//
+// Bytes bound it where there are many: 20304 rows of 64 heads on 8 of 128, bf16,
+// 642 MB in 128 us (5.0 TB/s, a plain copy's rate; keys and values alone 38 us,
+// 12 of them the 64-bit rotation, which hides behind the queries' bytes).  2112
+// rows of 32 heads on 8, fp32, 74 MB in 17.3 us; a decode step of 32 rows 5 us,
+// the chain row -> sequence -> page -> scale -> store.
 #include "kv_append.hpp"
 
 namespace lora {
@@ -68,8 +74,8 @@ __device__ __forceinline__ uint2 again8(uint2 v, float by) {   // by <= 1
 // s has room for its blocks from block_at(s) on, (rows before it) / block_size
 // and `per` more for each sequence before it.  n rows lie in n / block_size + 2
 // blocks at most, a single one in one.
-__device__ __forceinline__ int block_at(const AppendArgs& a, int s) {
-    return (a.B.row_off[s] >> a.S.block_shift) + a.S.per * s;
+__device__ __forceinline__ int block_at(const AppendArgs& a, int s, int first_row) {
+    return (first_row >> a.S.block_shift) + a.S.per * s;
 }
 
 // NP passes of a wave hold its part of a block; WPU waves share one.
@@ -84,44 +90,21 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     const bool is_v = hv >= n_heads;
     const int h = is_v ? hv - n_heads : hv;
 
-    // the sequence whose blocks `at` is among: the last one with block_at <= at
-    int s = 0, end = B.n_seqs;
-    while (s < end) {
-        const int step = (end - s + 63) >> 6;
-        const int i = s + (lane + 1) * step;
-        const bool le = i <= end && block_at(a, i) <= at;
-        const int c = __popcll(__ballot(le));
-        end = min(end, s + (c + 1) * step - 1);
-        s += c * step;
-    }
-    if (s >= B.n_seqs) return;
-    const int r0 = min(max(B.row_off[s], 0), B.n_rows), r1 = min(max(B.row_off[s + 1], r0), B.n_rows);
-    const int len = B.kv_len[s], first = len - (r1 - r0);   // tokens first .. len - 1 are new
+    // the sequence whose blocks `at` is among
+    int s, b0, b1, len;
+    if (!wave_find_seq(B, at, lane, [&](int i, int off) { return block_at(a, i, off); }, s, b0, b1, len)) return;
+    const int r0 = min(max(b0, 0), B.n_rows), r1 = min(max(b1, r0), B.n_rows);
+    const int first = len - (r1 - r0);   // tokens first .. len - 1 are new
     const int lo0 = max(first, 0);
-    const int t0 = ((lo0 >> a.S.block_shift) + (at - block_at(a, s))) << a.S.block_shift;
-    if (r1 == r0 || at < block_at(a, s) || t0 < 0 || t0 >= len) return;
+    const int t0 = ((lo0 >> a.S.block_shift) + (at - block_at(a, s, b0))) << a.S.block_shift;
+    if (r1 == r0 || at < block_at(a, s, b0) || t0 < 0 || t0 >= len) return;
     int before = 0;
     if (B.n_groups) {
         const int g = wave_find_run(B.group_off, B.n_groups, s, lane);
         if (g < B.n_groups) before = max(B.prefix_len[g], 0);
     }
-    const int pg = t0 >> a.C.page_shift;
-    const int page = pg < B.ldp ? B.pages[(int64_t)s * B.ldp + pg] : -1;
-    const int lo = max(t0, lo0);
-    int hi = min(t0 + (1 << a.S.block_shift), len);
-    if (a.cos) hi = min((int64_t)hi, (int64_t)a.n_pos - before);
-    if (page < 0 || page >= a.C.n_pages || first < 0 || hi < min(t0 + (1 << a.S.block_shift), len)) {
-        if (lane == 0 && part == 0 && a.status) flag_bad_id(a.status);
-        if (page < 0 || page >= a.C.n_pages) return;
-    }
-    if (hi <= lo) return;
-    const int cell = t0 & ((1 << a.C.page_shift) - 1);
-    uint8_t* to = (uint8_t*)(is_v ? a.C.v : a.C.k) + (int64_t)page * a.C.page_stride + (int64_t)h * a.C.head_stride +
-                  (int64_t)cell * a.C.token_stride;
-    float* scale = (is_v ? a.S.v_scale : a.S.k_scale) + (int64_t)page * a.S.page_stride +
-                   (int64_t)(cell >> a.S.block_shift) * a.S.block_stride + (int64_t)h * a.S.head_stride;
-    const bool kept = first > t0;   // earlier tokens share the block
-    const int was = kept ? min(max((int)((__float_as_uint(*scale) >> 23) & 255) - 127, Q8_LEAST), Q8_MOST) : 0;
+    const int lo = max(t0, lo0), all = min(t0 + (1 << a.S.block_shift), len);
+    const int hi = a.cos ? (int)min((int64_t)all, (int64_t)a.n_pos - before) : all;
 
     // this lane's place in every token: two pieces of 8, partners of one
     // another where heads are rotated in halves
@@ -132,7 +115,14 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     const int64_t ld = is_v ? a.ldv : a.ldk;
     const int token0 = part * NP * TPP + lane / LPT;   // of the block; a pass further on, TPP more
 
+    // the rows are requested before the place in the cache is looked up
     Eight<TI> x0[NP], x1[NP];
+    constexpr bool EARLY = NP <= 2;   // and so are their angles, where that leaves registers
+    Eight<float> cs[EARLY ? NP : 1], sn[EARLY ? NP : 1];
+    auto angles = [&](int t, int i) __attribute__((always_inline)) {
+        cs[i].load(a.cos + (int64_t)(before + t) * a.ldr + c * 8);
+        sn[i].load(a.sin + (int64_t)(before + t) * a.ldr + c * 8);
+    };
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int t = t0 + token0 + p * TPP;
@@ -140,19 +130,33 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
             const TI* src = from + (int64_t)(r0 + (t - first)) * ld;
             x0[p].load(src + e0);
             x1[p].load(src + e1);
+            if (EARLY && turn) angles(t, p);
         }
     }
+
+    const int pg = t0 >> a.C.page_shift;
+    const int page = pg < B.ldp ? B.pages[(int64_t)s * B.ldp + pg] : -1;
+    const bool page_ok = page >= 0 && page < a.C.n_pages;
+    if ((!page_ok || first < 0 || hi < all) && lane == 0 && part == 0 && a.status) flag_bad_id(a.status);
+    if (!page_ok || hi <= lo) return;
+    const int cell = t0 & ((1 << a.C.page_shift) - 1);
+    uint8_t* to = (uint8_t*)(is_v ? a.C.v : a.C.k) + (int64_t)page * a.C.page_stride + (int64_t)h * a.C.head_stride +
+                  (int64_t)cell * a.C.token_stride;
+    float* scale = (is_v ? a.S.v_scale : a.S.k_scale) + (int64_t)page * a.S.page_stride +
+                   (int64_t)(cell >> a.S.block_shift) * a.S.block_stride + (int64_t)h * a.S.head_stride;
+    const bool kept = first > t0;   // earlier tokens share the block
+    const int was = kept ? min(max((int)((__float_as_uint(*scale) >> 23) & 255) - 127, Q8_LEAST), Q8_MOST) : 0;
+
     float y0[NP][8], y1[NP][8], top = 0.f;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int t = t0 + token0 + p * TPP;
         if (!(t >= lo && t < hi)) continue;
         if (turn) {
-            Eight<float> cs, sn;
-            cs.load(a.cos + (int64_t)(before + t) * a.ldr + c * 8);
-            sn.load(a.sin + (int64_t)(before + t) * a.ldr + c * 8);
+            const int i = EARLY ? p : 0;
+            if (!EARLY) angles(t, 0);
             auto pair = [&](float p, float q, int e, float& u, float& w) __attribute__((always_inline)) {
-                const double P = p, Q = q, C = cs.get(e), S = sn.get(e);
+                const double P = p, Q = q, C = cs[i].get(e), S = sn[i].get(e);
                 u = to_odd(P * C - Q * S);
                 w = to_odd(P * S + Q * C);
             };
@@ -214,22 +218,22 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     }
 }
 
-// The queries' workgroups, then the blocks'.
+// The blocks' workgroups, whose chains are the longer ones, then the queries'.
 template <typename TI, int D, int NP, int WPU>
-__global__ __launch_bounds__(KA_WAVES * 64) void k_kv_append_q8(AppendArgs a, int it, int q_rows, int q_runs) {
+__global__ __launch_bounds__(KA_WAVES * 64) void k_kv_append_q8(AppendArgs a, int it, int q_runs) {
     __shared__ float sh[KA_WAVES];
-    const int q_blocks = q_rows * q_runs;
+    const int blocks = (int)((a.S.units * WPU + KA_WAVES - 1) / KA_WAVES);
     const int b = blockIdx.x;
-    if (b < q_blocks) {
-        append_row<TI, bf16, D>(a, it, b / q_runs, b % q_runs);
+    if (b >= blocks) {
+        append_row<TI, bf16, D, true>(a, it, (b - blocks) / q_runs, (b - blocks) % q_runs);
         return;
     }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (WPU == 1) {
-        const int64_t unit = (int64_t)(b - q_blocks) * KA_WAVES + wave;
+        const int64_t unit = (int64_t)b * KA_WAVES + wave;
         if (unit < a.S.units) append_block<TI, D, NP, 1>(a, unit, 0, sh);
     } else {
-        append_block<TI, D, NP, WPU>(a, b - q_blocks, wave, sh);
+        append_block<TI, D, NP, WPU>(a, b, wave, sh);
     }
 }
 
@@ -238,15 +242,19 @@ hipError_t launch_d(AppendArgs a, hipStream_t stream) {
     // whole keys and values of the heads, but for the row's part
     const int64_t q_rows = a.n_q_heads ? ceil_div(a.B.n_rows, KA_WAVES) : 0;
     const int chunks = (int)ceil_div((int64_t)a.n_q_heads * (D / 16), 64);
-    const int it = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)a.B.n_rows * chunks / 8192));
+    const int it = (int)std::max<int64_t>(1, std::min<int64_t>(chunks, (int64_t)a.B.n_rows * chunks / 2048));
     const int q_runs = a.n_q_heads ? (int)ceil_div(chunks, it) : 1;
+    // A wave takes a block of up to four passes by itself: four waves to such a
+    // block have four times the lookups (2112 rows in blocks of 32 of 128: 23.5
+    // us, one wave 17.3).  From eight passes on it would hold no registers for
+    // others (blocks of 64: 128 us, one wave 132).
     const int passes = (int)ceil_div((int64_t)D << a.S.block_shift, KQ_TOKENS);
     const int wpu = passes <= 4 ? 1 : KA_WAVES;
     const int64_t grid = q_rows * q_runs + ceil_div(a.S.units * wpu, KA_WAVES);
     if (grid >= (int64_t)1 << 31) return hipErrorInvalidValue;
     const dim3 g((unsigned)grid), block(KA_WAVES * 64);
 #define LORA_APPEND_Q8(NP, WPU) \
-    hipLaunchKernelGGL((k_kv_append_q8<TI, D, NP, WPU>), g, block, 0, stream, a, it, (int)q_rows, q_runs)
+    hipLaunchKernelGGL((k_kv_append_q8<TI, D, NP, WPU>), g, block, 0, stream, a, it, q_runs)
     switch (passes) {
         case 1: LORA_APPEND_Q8(1, 1); break;
         case 2: LORA_APPEND_Q8(2, 1); break;
