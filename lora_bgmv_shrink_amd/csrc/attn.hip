@@ -318,7 +318,15 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
             // would gain (32 of 4096: 83 / 93).  With thousands of pairs the
             // hardware's own order evens them out (512 of up to 8000: 1381 /
             // 1404), and there the shares' table would grow.
-            auto direct = [](int64_t u, int64_t pairs) {
+            // In 8 bits, units of 512 keys (lengths spread as above; whole / shares):
+            //     requests    1024         2048        4096        8192
+            //     1           13 / 16      17 / 16     26 / 17     51 / 21
+            //     8           13 / 17      21 / 20     32 / 29     54 / 34
+            //     16          15 / 19      21 / 28     33 / 32     56 / 47
+            //     32          17 / 28      23 / 36     38 / 48     70 / 79
+            //     64          29 / 38      42 / 53     74 / 82     132 / 135
+            auto direct = [in_8_bits](int64_t u, int64_t pairs) {
+                if (in_8_bits) return u <= 3 || (u <= 16 && pairs >= 16 * u) || pairs >= 4096;
                 return u <= 4 || (u <= 16 && pairs >= 8 * u) || pairs >= 4096;
             };
             W.few = direct(units, heads) ? 1 : 2;
