@@ -36,7 +36,8 @@ def rotary_tables(n_pos: int, rot_dim: int, device, base: float = 10000.0):
 class AttentionBlock:
     def __init__(self, d_model: int, n_q_heads: int, n_kv_heads: int, head_dim: int, n_adapters: int, rank: int,
                  dtype: torch.dtype, n_pages: int, page_size: int = 16, n_pos: int = 2048, window: int = 0,
-                 n_sink: int = 0, device="cuda", seed: int = 0):
+                 n_sink: int = 0, device="cuda", seed: int = 0, block_size: int = 0):
+        """``block_size`` > 0: keys and values in 8 bits, with a scale for that many tokens of a head."""
         g = torch.Generator().manual_seed(seed)
         self.hq, self.d, self.device, self.dtype = n_q_heads, head_dim, device, dtype
         self.wq, self.wk = n_q_heads * head_dim, n_kv_heads * head_dim
@@ -53,8 +54,18 @@ class AttentionBlock:
         self.w_qkv, self.qkv_pool = layer(d_model, self.wq + 2 * self.wk)
         self.w_o, self.o_pool = layer(self.wq, d_model)
         # one head's tokens of a page side by side; the binding sees [page, token, head, dim]
-        pages = [torch.zeros((n_pages, n_kv_heads, page_size, head_dim), dtype=dtype, device=device) for _ in range(2)]
-        self.cache = lb.KvCache(*(t.transpose(1, 2) for t in pages))
+        held = torch.uint8 if block_size else dtype
+        pages = [torch.zeros((n_pages, n_kv_heads, page_size, head_dim), dtype=held, device=device) for _ in range(2)]
+        k, v = (t.transpose(1, 2) for t in pages)
+        if block_size:
+            scales = [torch.ones((n_pages, page_size // block_size, n_kv_heads), device=device) for _ in range(2)]
+            self.cache = lb.KvCacheQ8(k.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn), *scales)
+            self.append, self.attend, self.workspace = lb.lora_kv_append_q8, lb.lora_attn_paged_q8, lb.attn_workspace_q8
+            self.attend_behind = lb.lora_attn_prefix_q8
+        else:
+            self.cache = lb.KvCache(k, v)
+            self.append, self.attend, self.workspace = lb.lora_kv_append, lb.lora_attn_paged, lb.attn_workspace
+            self.attend_behind = lb.lora_attn_prefix
         self.rope = lb.Rope(*rotary_tables(n_pos, head_dim, device))
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
@@ -62,8 +73,8 @@ class AttentionBlock:
         """The block over one step's rows ``x`` [n_rows, d_model]."""
         qkv = lb.lora_layer_apply(self.qkv_pool, x, self.w_qkv, ids, lb.LORA_W_OUT_IN, y_dtype=self.dtype)
         q, k, v = qkv.split([self.wq, self.wk, self.wk], dim=1)
-        q = lb.lora_kv_append(self.cache, batch, q, k, v, self.rope, q_out=q, status=self.status)
-        attend = lb.lora_attn_prefix if batch.n_groups else lb.lora_attn_paged
+        q = self.append(self.cache, batch, q, k, v, self.rope, q_out=q, status=self.status)
+        attend = self.attend_behind if batch.n_groups else self.attend
         o = attend(self.cache, batch, q, self.scale, window=self.window, n_sink=self.n_sink, status=self.status, ws=ws)
         return lb.lora_layer_apply(self.o_pool, o, self.w_o, ids, lb.LORA_W_OUT_IN, y_dtype=self.dtype)
 
@@ -93,7 +104,7 @@ class Server:
         self.decode_ids = torch.tensor(self.adapter, dtype=torch.int32, device=dev)
         n = len(self.prompt_len)
         self.decode_batch = self._requests([1] * n, max(counts))
-        self.decode_ws = lb.attn_workspace(block.cache, self.decode_batch, block.hq)
+        self.decode_ws = block.workspace(block.cache, self.decode_batch, block.hq)
 
     def _offsets(self, counts) -> torch.Tensor:
         return torch.cumsum(torch.tensor([0] + list(counts)), 0).to(torch.int32).to(self.block.device)
@@ -107,14 +118,14 @@ class Server:
         n = self.prefix_len
         batch = lb.KvBatch(self._offsets(n), self.prefix_dev, self.prefix_pages, sum(n), max(n), max(n))
         ids = torch.repeat_interleave(torch.arange(len(n)), torch.tensor(n)).to(torch.int32).to(self.block.device)
-        return self.block.step(x, ids, batch, lb.attn_workspace(self.block.cache, batch, self.block.hq))
+        return self.block.step(x, ids, batch, self.block.workspace(self.block.cache, batch, self.block.hq))
 
     def run_prompts(self, x: torch.Tensor) -> torch.Tensor:
         n = self.prompt_len
         per_group = [sum(r for r, a in zip(n, self.adapter) if a == g) for g in range(len(self.prefix_len))]
         batch = self._requests(n, max(per_group))
         ids = torch.repeat_interleave(self.decode_ids, self.kv_len.long())
-        return self.block.step(x, ids, batch, lb.attn_workspace(self.block.cache, batch, self.block.hq))
+        return self.block.step(x, ids, batch, self.block.workspace(self.block.cache, batch, self.block.hq))
 
     def run_decode(self, x: torch.Tensor) -> torch.Tensor:
         """One more token of every request (at most ``max_new`` times)."""
