@@ -670,9 +670,10 @@ def _here(t: Optional[torch.Tensor], cache: KvCache, dtype: torch.dtype) -> bool
     return t is None or (t.is_cuda and t.get_device() == cache.index and t.dtype == dtype and t.numel() > 0)
 
 
-def _append(fn, where: str, cache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+def _append(fn, where: str, kind, cache, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
             rope: Optional[Rope], q_out: Optional[torch.Tensor],
             status: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    assert isinstance(cache, kind), f"{where} takes a {kind.__name__}"
     n, d = batch.n_rows, cache.head_dim
     assert batch.index == cache.index and (rope is None or rope.index == cache.index), "tensors of the cache's device"
     assert k.dtype == v.dtype and _heads(k, cache, n) == cache.n_kv_heads == _heads(v, cache, n)
@@ -699,17 +700,18 @@ def lora_kv_append(cache: KvCache, batch: KvBatch, q: Optional[torch.Tensor], k:
     """Rotate the rows' q and k, write k and v into their pages and return
     the rotated q in the cache's type (``q_out``, allocated when not given;
     None without q)."""
-    return _append(_lib.lora_kv_append, "lora_kv_append", cache, batch, q, k, v, rope, q_out, status)
+    return _append(_lib.lora_kv_append, "lora_kv_append", KvCache, cache, batch, q, k, v, rope, q_out, status)
 
 
 def lora_kv_append_q8(cache: KvCacheQ8, batch: KvBatch, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                       rope: Optional[Rope] = None, q_out: Optional[torch.Tensor] = None,
                       status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """lora_kv_append into a cache in 8 bits; the rotated q is bf16."""
-    return _append(_lib.lora_kv_append_q8, "lora_kv_append_q8", cache, batch, q, k, v, rope, q_out, status)
+    return _append(_lib.lora_kv_append_q8, "lora_kv_append_q8", KvCacheQ8, cache, batch, q, k, v, rope, q_out, status)
 
 
 def lora_attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> int:
+    assert isinstance(cache, KvCache), "lora_attn_workspace takes a KvCache"
     v = ctypes.c_size_t()
     _check(_lib.lora_attn_workspace(cache.ref, batch.ref, n_q_heads, ctypes.byref(v)), "lora_attn_workspace")
     return v.value
@@ -723,6 +725,7 @@ def attn_workspace(cache: KvCache, batch: KvBatch, n_q_heads: int) -> torch.Tens
 
 
 def lora_attn_workspace_q8(cache: KvCacheQ8, batch: KvBatch, n_q_heads: int) -> int:
+    assert isinstance(cache, KvCacheQ8), "lora_attn_workspace_q8 takes a KvCacheQ8"
     v = ctypes.c_size_t()
     _check(_lib.lora_attn_workspace_q8(cache.ref, batch.ref, n_q_heads, ctypes.byref(v)), "lora_attn_workspace_q8")
     return v.value
@@ -733,9 +736,10 @@ def attn_workspace_q8(cache: KvCacheQ8, batch: KvBatch, n_q_heads: int) -> torch
     return torch.empty(lora_attn_workspace_q8(cache, batch, n_q_heads), dtype=torch.uint8, device=cache.device)
 
 
-def _attn(fn, where: str, workspace, cache, batch: KvBatch, q: torch.Tensor, scale: float, window: int, n_sink: int,
+def _attn(fn, where: str, kind, workspace, cache, batch: KvBatch, q: torch.Tensor, scale: float, window: int, n_sink: int,
           o: Optional[torch.Tensor], o_dtype: Optional[torch.dtype], lse: Optional[torch.Tensor],
           status: Optional[torch.Tensor], ws: Optional[torch.Tensor]) -> torch.Tensor:
+    assert isinstance(cache, kind), f"{where} takes a {kind.__name__}"
     n, d = batch.n_rows, cache.head_dim
     assert batch.index == cache.index, "tensors of the cache's device"
     hq = _heads(q, cache, n)
@@ -764,8 +768,8 @@ def lora_attn_paged(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: floa
                     ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of the batch's rows over their pages; ``lse`` [n_rows,
     n_q_heads] fp32 is filled when given."""
-    return _attn(_lib.lora_attn_paged, "lora_attn_paged", attn_workspace, cache, batch, q, scale, window, n_sink, o,
-                 o_dtype, lse, status, ws)
+    return _attn(_lib.lora_attn_paged, "lora_attn_paged", KvCache, attn_workspace, cache, batch, q, scale, window, n_sink,
+                 o, o_dtype, lse, status, ws)
 
 
 def lora_attn_prefix(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0, n_sink: int = 0,
@@ -774,8 +778,8 @@ def lora_attn_prefix(cache: KvCache, batch: KvBatch, q: torch.Tensor, scale: flo
                      ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """lora_attn_paged for a batch whose groups of sequences share a prefix,
     which a group's decode rows read once together."""
-    return _attn(_lib.lora_attn_prefix, "lora_attn_prefix", attn_workspace, cache, batch, q, scale, window, n_sink, o,
-                 o_dtype, lse, status, ws)
+    return _attn(_lib.lora_attn_prefix, "lora_attn_prefix", KvCache, attn_workspace, cache, batch, q, scale, window, n_sink,
+                 o, o_dtype, lse, status, ws)
 
 
 def lora_attn_paged_q8(cache: KvCacheQ8, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0,
@@ -783,8 +787,8 @@ def lora_attn_paged_q8(cache: KvCacheQ8, batch: KvBatch, q: torch.Tensor, scale:
                        lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                        ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """lora_attn_paged over a cache in 8 bits; q is bf16."""
-    return _attn(_lib.lora_attn_paged_q8, "lora_attn_paged_q8", attn_workspace_q8, cache, batch, q, scale, window,
-                 n_sink, o, o_dtype, lse, status, ws)
+    return _attn(_lib.lora_attn_paged_q8, "lora_attn_paged_q8", KvCacheQ8, attn_workspace_q8, cache, batch, q, scale,
+                 window, n_sink, o, o_dtype, lse, status, ws)
 
 
 def lora_attn_prefix_q8(cache: KvCacheQ8, batch: KvBatch, q: torch.Tensor, scale: float, window: int = 0,
@@ -792,8 +796,8 @@ def lora_attn_prefix_q8(cache: KvCacheQ8, batch: KvBatch, q: torch.Tensor, scale
                         lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                         ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """lora_attn_prefix over a cache in 8 bits; q is bf16."""
-    return _attn(_lib.lora_attn_prefix_q8, "lora_attn_prefix_q8", attn_workspace_q8, cache, batch, q, scale, window,
-                 n_sink, o, o_dtype, lse, status, ws)
+    return _attn(_lib.lora_attn_prefix_q8, "lora_attn_prefix_q8", KvCacheQ8, attn_workspace_q8, cache, batch, q, scale,
+                 window, n_sink, o, o_dtype, lse, status, ws)
 
 
 # --------------------------------------------------------------------------

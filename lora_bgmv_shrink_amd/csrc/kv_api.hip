@@ -22,6 +22,7 @@ bool ld16(int64_t ld, int eb) { return ld % (16 / eb) == 0; }
 lora_status_t dev_status(hipError_t e) { return e == hipSuccess ? LORA_OK : LORA_E_DEVICE; }
 
 constexpr int64_t kMost = (int64_t)1 << 30;   // rows, lengths, columns and table widths
+constexpr int64_t kMostUnits = (int64_t)1 << 23;   // of a launch that has a workgroup for each
 
 lora_status_t check_cache(const lora_kv_cache_t* c, KvDev& C) {
     if (!c || !dtype_ok(c->dtype) || !c->k || !c->v) return LORA_E_INVALID;
@@ -281,13 +282,18 @@ lora_status_t lora_kv_append_q8(const lora_kv_cache_q8_t* cache, const lora_kv_b
     std::memset(&a, 0, sizeof a);
     const lora_status_t st = check_cache_q8(cache, a.C, a.S);
     if (st != LORA_OK) return st;
-    if (batch && (int64_t)std::max(batch->n_seqs, 0) * cache->n_kv_heads > kMost) return LORA_E_UNSUPPORTED;
+    // (block, head, K or V) units, a workgroup each at most
+    const int per = batch && batch->max_rows <= 1 ? 1 : 2;
+    if (batch) {
+        const int64_t blocks = ((int64_t)std::max(batch->n_rows, 0) >> a.S.block_shift) +
+                               (int64_t)per * std::max(batch->n_seqs, 0);
+        a.S.per = per;
+        a.S.units = blocks * 2 * cache->n_kv_heads;
+        if (blocks > kMostUnits || a.S.units > kMostUnits) return LORA_E_UNSUPPORTED;
+    }
     return run_append(a, cache->n_kv_heads, cache->head_dim, 2, batch, rope, dtype, q, ldq, n_q_heads, k, ldk, v, ldv,
                       q_out, ldqo, status, [&] {
                           a.C.n_kv_heads = 0;   // the queries' part writes no keys and values
-                          a.S.per = batch->max_rows <= 1 ? 1 : 2;
-                          a.S.units = (((int64_t)batch->n_rows >> a.S.block_shift) + (int64_t)a.S.per * batch->n_seqs) *
-                                      2 * cache->n_kv_heads;
                           return launch_kv_append_q8(a, dtype, cache->head_dim, stream);
                       });
 }

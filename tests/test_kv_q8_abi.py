@@ -111,6 +111,12 @@ def test_append_refusals():
     assert append(b, cache, batch, rope, k=None, v=None, q=None, qo=None) == b.LORA_OK
     batch.n_rows, batch.n_seqs, cache.n_kv_heads = 5, 1 << 24, 1 << 10
     assert append(b, cache, batch, rope, ldk=1 << 20, ldv=1 << 20) == U
+    _, cache, batch, rope = structs()
+    for field in ("n_rows", "n_seqs"):   # more blocks than a launch has workgroups
+        _, cache, batch, rope = structs()
+        cache.block_size = 1
+        setattr(batch, field, 1 << 26)
+        assert append(b, cache, batch, rope) == U, field
 
 
 def plan_struct(b):
@@ -204,3 +210,25 @@ def test_plan_binding(b, monkeypatch):
         b.lora_kv_plan(plan, ints(1, 1), status=ints(0).long())
     assert rec.calls == 0
     assert b.lora_kv_plan(plan, ints(1, 1), ints(0, 0)) is plan and rec.calls == 1
+
+
+def test_caches_are_not_mixed_up(b, monkeypatch):
+    """The two caches are different structures: an entry point of one refuses the other's."""
+    rec = Recorder()
+    eight_bits = b.KvCacheQ8(eight(5, 16, 2, 64), eight(5, 16, 2, 64), floats(5, 4, 2), floats(5, 4, 2))
+    wide = b.KvCache(*(OnDevice.of(torch.zeros((5, 16, 2, 64), dtype=torch.bfloat16)) for _ in range(2)))
+    batch = b.KvBatch(ints(0, 1), ints(5), ints([0]), 1, 1, 5)
+    q, k = (OnDevice.of(torch.zeros((1, n), dtype=torch.bfloat16)) for n in (256, 128))
+    monkeypatch.setattr(b, "_lib", rec)
+    for cache, fns in ((wide, (b.lora_attn_paged_q8, b.lora_attn_prefix_q8)), (eight_bits, (b.lora_attn_paged, b.lora_attn_prefix))):
+        for fn in fns:
+            with pytest.raises(AssertionError, match="takes a KvCache"):
+                fn(cache, batch, q, 0.1)
+    for cache, fns in ((wide, (b.lora_kv_append_q8,)), (eight_bits, (b.lora_kv_append,))):
+        for fn in fns:
+            with pytest.raises(AssertionError, match="takes a KvCache"):
+                fn(cache, batch, q, k, k)
+    for fn, cache in ((b.lora_attn_workspace, eight_bits), (b.lora_attn_workspace_q8, wide)):
+        with pytest.raises(AssertionError, match="takes a KvCache"):
+            fn(cache, batch, 4)
+    assert rec.calls == 0
