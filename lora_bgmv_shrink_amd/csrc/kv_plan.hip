@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * NW) void k_plan(PlanArgs a) {
             all_back = sat_add(all_back, total[0]);
         }
     }
-    int asked[3] = {0, 0, 0}, given[2] = {0, 0};   // before this round's sequences
+    int asked[3] = {0, 0, 0}, given[2] = {0, 0};   // before this pass's sequences
     bool refused = false;
     for (int s0 = 0; s0 < n; s0 += T) {
         const int s = s0 + tid;
