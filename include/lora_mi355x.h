@@ -851,7 +851,8 @@ typedef struct {
  * the block held tokens of the sequence before, no less than it was, and if it
  * grows those tokens are rounded again to the new one (which drops bits only
  * of values that fall below 2^-6 of the scale).  Infinities and NaN become NaN
- * and do not count for the scale; values past 448 * 2^100 become that. */
+ * and do not count for the scale; values past 448 * 2^100 become that.
+ * (n_rows / block_size + 2 n_seqs) * 2 n_kv_heads: at most 2^23. */
 lora_status_t lora_kv_append_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, const lora_rope_t* rope,
                                 lora_dtype_t dtype, const void* q, int64_t ldq, int32_t n_q_heads, const void* k,
                                 int64_t ldk, const void* v, int64_t ldv, void* q_out, int64_t ldqo, int32_t* status,

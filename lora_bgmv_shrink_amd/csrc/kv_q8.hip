@@ -95,6 +95,8 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     if (!wave_find_seq(B, at, lane, [&](int i, int off) { return block_at(a, i, off); }, s, b0, b1, len)) return;
     const int r0 = min(max(b0, 0), B.n_rows), r1 = min(max(b1, r0), B.n_rows);
     const int first = len - (r1 - r0);   // tokens first .. len - 1 are new
+    // more rows than tokens: the first ones have no place (nor any, without tokens)
+    if (r1 > r0 && first < 0 && lane == 0 && part == 0 && a.status) flag_bad_id(a.status);
     const int lo0 = max(first, 0);
     const int t0 = ((lo0 >> a.S.block_shift) + (at - block_at(a, s, b0))) << a.S.block_shift;
     if (r1 == r0 || at < block_at(a, s, b0) || t0 < 0 || t0 >= len) return;
@@ -137,7 +139,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     const int pg = t0 >> a.C.page_shift;
     const int page = pg < B.ldp ? B.pages[(int64_t)s * B.ldp + pg] : -1;
     const bool page_ok = page >= 0 && page < a.C.n_pages;
-    if ((!page_ok || first < 0 || hi < all) && lane == 0 && part == 0 && a.status) flag_bad_id(a.status);
+    if ((!page_ok || hi < all) && lane == 0 && part == 0 && a.status) flag_bad_id(a.status);
     if (!page_ok || hi <= lo) return;
     const int cell = t0 & ((1 << a.C.page_shift) - 1);
     uint8_t* to = (uint8_t*)(is_v ? a.C.v : a.C.k) + (int64_t)page * a.C.page_stride + (int64_t)h * a.C.head_stride +

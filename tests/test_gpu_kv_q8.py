@@ -632,6 +632,25 @@ def test_append_refuses_places():
         check_append(c, cache, "places")
 
 
+@pytest.mark.parametrize("nq,ln", [([3], [0]), ([1, 2], [5, 0]), ([2, 1], [-4, 9])], ids=str)
+def test_rows_of_a_sequence_without_tokens(nq, ln):
+    """No row of it has a place: reported, with queries and without, and nothing of the cache changes for it."""
+    b = binding()
+    for with_q in (True, False):
+        c = CaseQ8(nq, [max(n, 0) for n in ln], 2, 1, 64, page=16, block=8, seed=38)
+        cache, batch = c.cache(b), c.batch(b)
+        batch.tensors[1].copy_(torch.tensor(ln, dtype=torch.int32))
+        x = torch.randn((c.n_rows, 128)).to(BF)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        say(f"rows {nq} of sequences of {ln} tokens, {'q' if with_q else 'no q'}")
+        k = x[:, :64].contiguous()
+        b.lora_kv_append_q8(cache, batch, x.to(DEV) if with_q else None, k.to(DEV), k.to(DEV), status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 1
+        _kv_q8.append(c, {"k": k, "v": k})
+        check_append(c, cache, "no tokens")
+
+
 def test_many_idle_sequences():
     """The blocks' numbering skips sequences without rows, and a batch whose bound is one row."""
     b = binding()
