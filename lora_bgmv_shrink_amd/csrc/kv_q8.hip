@@ -6,18 +6,19 @@
 //
 // x the rotated key or the value.  A number has 4 significant bits, so a
 // rotation rounded before it is rounded again may end on the wrong side of a
-// tie: keys are rotated in 64 bits (a product of two fp32 is exact there) and
-// brought to fp32 by rounding to odd, which keeps what the last rounding has
-// to know.  A power of two as scale costs no rounding of its own, keeps the
-// earlier tokens' bits when it grows (but below 2^-6 of it), and is what the
-// matrix cores' widening takes.
+// tie: a key's two products are made in 64 bits (of two fp32 numbers each is
+// exact there), and their sum, with what 64 bits leave of it where that may
+// count, is brought to fp32 by rounding to odd, which keeps what the last
+// rounding has to know.  A power of two as scale costs no rounding of its own,
+// keeps the earlier tokens' bits when it grows (but below 2^-6 of it), and is
+// what the matrix cores' widening takes.
 //
 // Queries go the way of the other caches, rounded to bf16.
 //
 // Bytes bound it where there are many: 20304 rows of 64 heads on 8 of 128, bf16,
-// 642 MB in 128 us (5.0 TB/s, a plain copy's rate; keys and values alone 38 us,
+// 642 MB in 130 us (4.9 TB/s, nearly a plain copy's rate; keys and values alone 38 us,
 // 12 of them the 64-bit rotation, which hides behind the queries' bytes).  2112
-// rows of 32 heads on 8, fp32, 74 MB in 17.3 us; a decode step of 32 rows 5 us,
+// rows of 32 heads on 8, fp32, 74 MB in 17.2 us; a decode step of 32 rows 5 us,
 // the chain row -> sequence -> page -> scale -> store.
 #include "kv_append.hpp"
 
@@ -36,6 +37,20 @@ __device__ __forceinline__ float to_odd(double x) {
     int bits = __float_as_int(f);
     if (b != x && !(bits & 1)) bits += fabs(b) < fabs(x) ? 1 : -1;
     return __int_as_float(bits);
+}
+// Ties of two numbers, and the border of two scales, have 5 significant bits at
+// the most.  Where to_odd(a + b) has no more, the sum in 64 bits is that
+// number, and a + b may be next to it by less than 64 bits tell.
+__device__ __forceinline__ uint32_t low_bits(float y) { return __float_as_uint(y) << 13; }
+// On which side of the sum in 64 bits a + b lies: 1 the larger magnitude's, 2
+// the smaller one's, 0: it is that sum.
+__device__ __forceinline__ uint32_t side_of(double a, double b) {
+    const double x = a + b, t = x - a, rest = (a - (x - t)) + (b - t);   // NaN where x is infinite
+    return rest < 0. || rest > 0. ? ((rest > 0.) == (x > 0.) ? 1u : 2u) : 0u;
+}
+// y = to_odd(a + b), its last bit set for that side
+__device__ __forceinline__ float to_side(float y, uint32_t side) {
+    return __int_as_float(__float_as_int(y) + (low_bits(y) == 0 ? (int)(side & 1) - (int)(side >> 1 & 1) : 0));
 }
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
 
@@ -150,6 +165,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     const int was = kept ? min(max((int)((__float_as_uint(*scale) >> 23) & 255) - 127, Q8_LEAST), Q8_MOST) : 0;
 
     float y0[NP][8], y1[NP][8], top = 0.f;
+    uint32_t low = ~0u;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int t = t0 + token0 + p * TPP;
@@ -161,6 +177,7 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
                 const double P = p, Q = q, C = cs[i].get(e), S = sn[i].get(e);
                 u = to_odd(P * C - Q * S);
                 w = to_odd(P * S + Q * C);
+                low = min(low, min(low_bits(u), low_bits(w)));
             };
             if (halves) {
 #pragma unroll
@@ -183,6 +200,33 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
         for (int e = 0; e < 8; ++e) {
             top = fmaxf(top, finite(y0[p][e]) ? fabsf(y0[p][e]) : 0.f);
             top = fmaxf(top, finite(y1[p][e]) ? fabsf(y1[p][e]) : 0.f);
+        }
+    }
+    if (low == 0) {
+        // A pair at a time, from memory: nothing is held for it (with whole sums
+        // in any case 2112 fp32 rows take 20.6 us, so 17.2).  The top stays: a
+        // border that the last bit is set below calls for the same scale.
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int t = t0 + token0 + p * TPP;
+            if (!(t >= lo && t < hi)) continue;
+            const TI* src = from + (int64_t)(r0 + (t - first)) * ld;
+            const int64_t angle = (int64_t)(before + t) * a.ldr + c * 8;
+            uint32_t sides[2] = {0, 0};
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                const int ea = halves ? e0 + k : e0 + 2 * k, eb = halves ? e1 + k : ea + 1;
+                const double P = to_f32(src[ea]), Q = to_f32(src[eb]), C = a.cos[angle + k], S = a.sin[angle + k];
+                sides[0] |= side_of(P * C, -(Q * S)) << (2 * k);
+                sides[1] |= side_of(P * S, Q * C) << (2 * k);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y0[p][e] = to_side(y0[p][e], halves ? sides[0] >> (2 * e) : sides[e & 1] >> (e & 6));
+                y1[p][e] = to_side(y1[p][e], halves ? sides[1] >> (2 * e) : sides[e & 1] >> (8 + (e & 6)));
+                if (finite(y0[p][e])) top = fmaxf(top, fabsf(y0[p][e]));
+                if (finite(y1[p][e])) top = fmaxf(top, fabsf(y1[p][e]));
+            }
         }
     }
 #pragma unroll
