@@ -852,6 +852,10 @@ typedef struct {
  * grows those tokens are rounded again to the new one (which drops bits only
  * of values that fall below 2^-6 of the scale).  Infinities and NaN become NaN
  * and do not count for the scale; values past 448 * 2^100 become that.
+ * With max_rows at most 1, a sequence of n rows from row r on has room for
+ * (r + n) / block_size - r / block_size + 1 blocks, which is enough where the
+ * bound holds; where it does not, its blocks past them are not written and
+ * status gets bit 0 set.  With a larger max_rows every row has room.
  * (n_rows / block_size + 2 n_seqs) * 2 n_kv_heads: at most 2^23. */
 lora_status_t lora_kv_append_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, const lora_rope_t* rope,
                                 lora_dtype_t dtype, const void* q, int64_t ldq, int32_t n_q_heads, const void* k,

@@ -1,5 +1,6 @@
 """What append writes to a cache in 8 bits, against rationals: rotated keys whose exact value lies next to a tie of two
-numbers, or next to the border of two scales, by far less than 53 bits tell.  Every number has to be the same."""
+numbers, or next to the border of two scales, by far less than 53 bits tell; and rows past the batch's bound.  Every
+number has to be the same."""
 from __future__ import annotations
 
 from fractions import Fraction
@@ -95,3 +96,42 @@ def test_next_to_ties_and_borders(given, interleaved, d, page, block, top_by):
     got = cache.k.view(torch.uint8)[pg, :4, 0].cpu()
     far = (got != want).nonzero().tolist()
     assert not far, [(t, i, float(y[t][i]), int(got[t, i]), int(want[t, i])) for t, i in far[:5]]
+
+
+@pytest.mark.parametrize("page,block", [(16, 4), (8, 1), (16, 16), (128, 64), (128, 128)])
+@pytest.mark.parametrize("most", [0, 1, 3])
+@pytest.mark.parametrize("with_q", [False, True])
+def test_rows_past_the_bound(page, block, most, with_q):
+    """max_rows below what sequences bring: rows that have no room for it are reported and the others written, all of
+    them with a bound of more than a row."""
+    b = binding()
+    c = CaseQ8([3, 1, 0, 90, 2], [17, 4, 7, 95, 129], 4, 2, 64, page=page, block=block, seed=51)
+    cache, full = c.cache(b), c.batch(b)
+    batch = b.KvBatch(*full.tensors[:3], c.n_rows, most, max(c.kv_len))
+    g = torch.Generator().manual_seed(52)
+    x = {i: torch.randn((c.n_rows, 128), generator=g).to(torch.bfloat16) for i in "kv"}
+    q = torch.randn((c.n_rows, 256), generator=g).to(torch.bfloat16).to(DEV) if with_q else None
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    say(f"rows past a bound of {most}: page {page} block {block}")
+    out = b.lora_kv_append_q8(cache, batch, q, x["k"].to(DEV), x["v"].to(DEV), status=status)
+    torch.cuda.synchronize()
+    before = [[t.clone() for t in y] for y in (c.codes, c.scales)]
+    assert _kv_q8.append(c, x) == list(range(c.n_rows))
+    lost, starts = 0, c.starts()
+    for s, (n, length) in enumerate(zip(c.nq, c.kv_len)):
+        room = starts[s + 1] // block - starts[s] // block + (1 if most <= 1 else 2)
+        for t0 in list(range((length - n) // block * block, length, block))[room:] if n else []:
+            pg, at = c.pages[s][t0 // page], t0 % page
+            lost += 1
+            for i in (0, 1):
+                c.codes[i][pg, at:at + block] = before[0][i][pg, at:at + block]
+                c.scales[i][pg, at // block] = before[1][i][pg, at // block]
+    assert int(status.item()) == (1 if lost else 0)
+    assert bool(lost) == (most <= 1 and block > 1)
+    for i, name in enumerate("kv"):
+        got, want = getattr(cache, name).view(torch.uint8).cpu(), c.codes[i]
+        nan = (want & 127) == 127
+        assert torch.equal((got & 127) == 127, nan) and torch.equal(got[~nan], want[~nan]), name
+        scales = getattr(cache, name + "_scale").double().cpu()
+        assert torch.equal(torch.nan_to_num(scales, 7.0), torch.nan_to_num(c.scales[i], 7.0)), name
+    assert q is None or torch.equal(out, q)
