@@ -32,10 +32,12 @@ from lora_bgmv_shrink_amd import binding as lb  # noqa: E402
 
 
 class Steps:
-    """Steps of up to ``max_rows`` rows, ``most`` of them one request's, over ``n_places`` places."""
+    """Steps of up to ``max_rows`` rows, ``most`` of them one request's, over ``n_places`` places.  A request has up
+    to ``max_len`` tokens, rounded up to whole pages."""
 
     def __init__(self, block: AttentionBlock, n_places: int, max_rows: int, most: int, max_len: int):
         self.block, dev, page = block, block.device, block.cache.page_size
+        self.most, self.max_rows = most, max_rows
 
         def ints(n, value=0):
             return torch.full((n,), value, dtype=torch.int32, device=dev)
@@ -44,8 +46,9 @@ class Steps:
         pages = torch.full((n_places, -(-max_len // page)), -1, dtype=torch.int32, device=dev)
         free = torch.arange(block.cache.n_pages, dtype=torch.int32, device=dev)
         self.plan = lb.KvPlan(ints(n_places), pages, free, ints(1, block.cache.n_pages), page, max_rows)
-        # the tensors that every step's plan writes
-        self.batch = lb.KvBatch(self.plan.row_off, self.plan.kv_len, self.plan.pages, max_rows, most, max_len)
+        # the tensors that every step's plan writes; bounds that hold for all that it may grant (a whole table's
+        # tokens), as what is past them would be neither computed nor seen.  `most` is checked by step()
+        self.batch = lb.KvBatch(self.plan.row_off, self.plan.kv_len, self.plan.pages, max_rows, most, pages.shape[1] * page)
         self.ws = block.workspace(block.cache, self.batch, block.hq)
         # rows as they are brought, place by place, the first of each place, and one past the last for the rows of a
         # step that are nobody's
@@ -77,6 +80,8 @@ class Steps:
     def step(self, new_rows: List[int], adapter: List[int], x: torch.Tensor) -> torch.Tensor:
         """One step: place i brings new_rows[i] rows (below zero: its request is over); ``x`` are the rows, in the
         order of their places.  Returns theirs of the output, zeros where the place was not served."""
+        if max(new_rows) > self.most or sum(max(n, 0) for n in new_rows) > min(self.max_rows, x.shape[0]):
+            raise ValueError(f"more rows than {self.most} of a request, {self.max_rows} of a step, or {x.shape[0]} brought")
         first = torch.tensor([0] + new_rows).clamp(min=0).cumsum(0)
         self.first.copy_(first[:-1])
         self.new_rows.copy_(torch.tensor(new_rows, dtype=torch.int32))

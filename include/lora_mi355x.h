@@ -796,6 +796,9 @@ lora_status_t lora_attn_prefix(const lora_kv_cache_t* cache, const lora_kv_batch
  * all of them, and no place.
  *   status (may be NULL) gets bit 0 set when a sequence was refused, bit 1
  *   when more pages came back than the stack holds (the last are dropped).
+ * A lora_kv_batch_t over these tables needs bounds that hold for what is
+ * granted: its max_kv_len for ldp * page_size tokens (or fewer, where new_rows
+ * keeps to it), its max_rows for the largest of new_rows that fits this max_rows.
  * page_size: a power of two; n_seqs at most 2^20.  Contents that break these
  * rules give unspecified values, but nothing outside the arrays is read or
  * written.  One launch for steps of up to 1024 sequences and 4096 rows,

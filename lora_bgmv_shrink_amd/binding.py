@@ -811,7 +811,9 @@ class KvPlan:
     all updated in place by every step; ``kv_len_out`` and ``n_free_out``
     leave the old lengths and height as they are), and the step's tables, which
     every call writes: ``row_off`` [n_seqs + 1], ``row_seq``, ``row_adapter``,
-    ``row_pos`` [max_rows] int32 and ``row_slot`` [max_rows] int64."""
+    ``row_pos`` [max_rows] int32 and ``row_slot`` [max_rows] int64.  A KvBatch
+    over them needs bounds that hold for what is granted: ``pages.shape[1] *
+    page_size`` tokens and the largest of ``new_rows``."""
 
     def __init__(self, kv_len: torch.Tensor, pages: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor,
                  page_size: int, max_rows: int, kv_len_out: Optional[torch.Tensor] = None,

@@ -1,4 +1,4 @@
-"""The example's steps when the plan serves some requests and not others."""
+"""The example's steps when the plan serves some requests and not others, and at the bounds of its batch."""
 from __future__ import annotations
 
 import pytest
@@ -69,3 +69,29 @@ def test_who_was_served():
     for i, (new, want) in enumerate((([5, 0, 4], [True] * 3), ([1, 30, 1], [True, False, True]), ([1, -1, -1], [True] * 3))):
         run(steps, i, new)
         assert steps.served() == want, i
+
+
+def test_requests_as_long_as_their_tables():
+    """max_len is rounded up to whole pages: what the plan grants, the attention sees."""
+    tight, roomy = new_steps(8, 20, places=1), new_steps(8, 64, places=1)
+    assert tight.plan.pages.shape[1] == 2
+    say("up to the table's end")
+    for i, n in enumerate([20] + [1] * 12):
+        a, b = run(tight, i, [n])[0], run(roomy, i, [n])[0]
+        assert torch.equal(a, b), f"step {i}"
+    assert int(tight.plan.kv_len) == 32 and int(tight.block.status) == 0
+    run(tight, 20, [1])
+    assert int(tight.plan.kv_len) == 32 and int(tight.block.status) == 1
+
+
+def test_more_rows_than_a_step_takes():
+    """Rows that the attention's bound or the step does not cover are turned away, and nothing has changed."""
+    steps = new_steps(20, 200, most=30, max_rows=64)
+    run(steps, 0, [30, 4, 30])
+    lens = steps.plan.kv_len.tolist()
+    say("too many rows")
+    for new, x in (([31, 0, 0], 31), ([30, 5, 30], 65), ([3, 0, 2], 4)):
+        with pytest.raises(ValueError):
+            steps.step(new, [0, 1, 2], torch.zeros((x, 256), dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    assert steps.plan.kv_len.tolist() == lens == [30, 4, 30]
