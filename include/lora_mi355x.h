@@ -785,7 +785,10 @@ lora_status_t lora_attn_prefix(const lora_kv_cache_t* cache, const lora_kv_batch
  * their tables left out, are more than max_rows; or when it needs pages and
  * these and the ones that those sequences need are more than there are.  So
  * what a refused request asked for is not given to a later one, but a later one
- * that needs no page is served.
+ * that needs no page is served.  A sequence that asks for more than there can
+ * ever be keeps those behind it waiting for good: with more than max_rows rows
+ * all of them, with more pages than the server has those that need pages.  A
+ * long prompt is brought in pieces of up to max_rows rows.
  * Written:
  *   row_off[n_seqs + 1]  rows of sequence s: row_off[s] .. row_off[s + 1] - 1
  *                        (none where it was refused);
