@@ -736,6 +736,10 @@ lora_status_t lora_kv_append(const lora_kv_cache_t* cache, const lora_kv_batch_t
  *   Scores, softmax statistics and sums are fp32; the weights are rounded to
  *   the cache's type before the product with V, and o once at the end (so an
  *   fp32 o of a bf16 cache still has the weights' rounding, 2^-8 of each).
+ *   A weight before the division may be up to 2^20, so a sum may reach 2^20
+ *   times the number of keys times the largest value: with values of up to
+ *   2^77 in magnitude it never leaves fp32's range, with larger ones it may,
+ *   and o is then infinite or NaN.
  *   status (device, may be NULL) gets bit 0 set when a page number that some
  *   row needs is outside [0, n_pages); its tokens are then not seen.
  * Results do not depend on timing.  lora_attn_paged takes a batch without
@@ -871,7 +875,8 @@ lora_status_t lora_kv_append_q8(const lora_kv_cache_q8_t* cache, const lora_kv_b
 /* lora_attn_workspace, lora_attn_paged and lora_attn_prefix over a cache in 8
  * bits; q is bf16.  Keys and values are widened to bf16, which holds an e4m3
  * number times a power of two as it is: results are those of a bf16 cache
- * that holds the same numbers, up to the order of sums. */
+ * that holds the same numbers, up to the order of sums (and up to its limit on
+ * the size of values: a scale of V of up to 2^68 keeps to it). */
 lora_status_t lora_attn_workspace_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, int32_t n_q_heads,
                                      size_t* bytes);
 lora_status_t lora_attn_paged_q8(const lora_kv_cache_q8_t* cache, const lora_kv_batch_t* batch, const void* q,
