@@ -325,6 +325,19 @@ void plan_attn(AttnPlan& P, int32_t head_dim, int32_t elem_bytes, const int32_t 
             //     16          15 / 19      21 / 28     33 / 32     56 / 47
             //     32          17 / 28      23 / 36     38 / 48     70 / 79
             //     64          29 / 38      42 / 53     74 / 82     132 / 135
+            // The same rule for units of 256 keys: heads of 256 (whole / shares),
+            //     requests    512       768       1024      2048      4096      8192
+            //     1           16 / 19   20 / 19   23 / 19   38 / 21   63 / 26   111 / 35
+            //     8           16 / 20   20 / 22   25 / 22   41 / 38   70 / 54   116 / 64
+            //     16          17 / 22   22 / 35   25 / 36   41 / 56   68 / 64   120 / 94
+            //     32          19 / 35   23 / 46   27 / 52   40 / 63   74 / 95   132 / 136
+            //     64          34 / 53   41 / 62   48 / 67   84 / 105  137 / 147
+            // and of 128 beside a prompt of 40 rows, in one launch:
+            //     1           15 / 17   15 / 17   15 / 17   21 / 18   34 / 20   61 / 25
+            //     8           15 / 17   15 / 18   16 / 19   24 / 29   37 / 36   63 / 42
+            //     16          13 / 18   13 / 19   14 / 19   21 / 34   34 / 37   61 / 54
+            //     32          26 / 30   28 / 41   31 / 42   37 / 50   52 / 64   85 / 94
+            //     64          36 / 40   39 / 50   43 / 53   57 / 68   89 / 98
             auto direct = [in_8_bits](int64_t u, int64_t pairs) {
                 if (in_8_bits) return u <= 3 || (u <= 16 && pairs >= 16 * u) || pairs >= 4096;
                 return u <= 4 || (u <= 16 && pairs >= 8 * u) || pairs >= 4096;
