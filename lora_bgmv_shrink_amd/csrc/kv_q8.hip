@@ -208,8 +208,8 @@ __device__ __forceinline__ void append_block(const AppendArgs& a, int64_t unit, 
     }
     if (low == 0) {
         // A pair at a time, from memory: nothing is held for it (with whole sums
-        // in any case 2112 fp32 rows take 20.6 us, so 17.2).  The top stays: a
-        // border that the last bit is set below calls for the same scale.
+        // in any case 2112 fp32 rows take 20.6 us, so 17.2).  top only grows:
+        // for a sum just below a border the border's own scale is right too.
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int t = t0 + token0 + p * TPP;
